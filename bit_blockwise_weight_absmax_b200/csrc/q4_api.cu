@@ -4,7 +4,6 @@
 // status codes.  Every step of the computation runs in the sm_100a kernels of
 // the other translation units; the host never touches tensor data and never
 // allocates device memory.
-#include <cuda.h>
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
@@ -23,7 +22,74 @@ __device__ int g_status = 0;
 std::atomic<uint64_t> g_wait_limit_ns{kWaitLimitNs};
 // Test hook of the bounded waits: the GEMV copy warps issue no copies.
 std::atomic<int32_t> g_copy_stall{0};
+
+DeviceInfo device_info() {
+  static DeviceInfo cache[64];
+  static bool filled[64] = {};
+  static std::mutex mu;
+  int count = 0;
+  if (cudaGetDeviceCount(&count) != cudaSuccess || count == 0) {
+    cudaGetLastError();
+    return DeviceInfo{};
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DeviceInfo{Q4_ERR_CUDA, 0, nullptr};
+  std::lock_guard<std::mutex> lk(mu);
+  if (filled[dev]) return cache[dev];
+  DeviceInfo d;
+  int major = 0, minor = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || d.sms < 1) {
+    cudaGetLastError();
+    return DeviceInfo{Q4_ERR_CUDA, 0, nullptr};  // not cached: a later call asks again
+  }
+  d.ok = (major == 10 && minor == 0) ? Q4_OK : Q4_ERR_ARCH;
+  if (d.ok == Q4_OK) {
+    void *ptr = nullptr;
+    if (cudaGetSymbolAddress(&ptr, q4::g_status) != cudaSuccess) {
+      cudaGetLastError();
+      d.ok = Q4_ERR_CUDA;
+    }
+    d.status = reinterpret_cast<int *>(ptr);
+  }
+  cache[dev] = d;
+  filled[dev] = true;
+  return d;
 }
+// ---- TMA descriptors ----------------------------------------------------------------
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+    cudaGetLastError();
+  });
+  return fn;
+}
+
+// 2-D row-major tensor [rows, cols] of `esize`-byte elements, rows
+// `stride_bytes` apart (0: packed), box {bx, by}.
+bool make_map(CUtensorMap *m, CUtensorMapDataType dt, const void *base, int64_t rows, int64_t cols,
+              int esize, int bx, int by, CUtensorMapSwizzle sw, int64_t stride_bytes) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(stride_bytes ? stride_bytes : cols * esize)};
+  const cuuint32_t box[2] = {(cuuint32_t)bx, (cuuint32_t)by};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace q4
 
 using namespace q4;
 
@@ -82,47 +148,6 @@ bool build_bin_table(Nf4BinTable *tab) {
   return true;
 }
 
-struct DeviceInfo {
-  int ok = Q4_ERR_NO_DEVICE;
-  int sms = 0;
-  int *status = nullptr;  // device address of q4::g_status
-};
-
-DeviceInfo device_info() {
-  static DeviceInfo cache[64];
-  static bool filled[64] = {};
-  static std::mutex mu;
-  int count = 0;
-  if (cudaGetDeviceCount(&count) != cudaSuccess || count == 0) {
-    cudaGetLastError();
-    return DeviceInfo{};
-  }
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DeviceInfo{Q4_ERR_CUDA, 0, nullptr};
-  std::lock_guard<std::mutex> lk(mu);
-  if (filled[dev]) return cache[dev];
-  DeviceInfo d;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || d.sms < 1) {
-    cudaGetLastError();
-    return DeviceInfo{Q4_ERR_CUDA, 0, nullptr};  // not cached: a later call asks again
-  }
-  d.ok = (major == 10 && minor == 0) ? Q4_OK : Q4_ERR_ARCH;
-  if (d.ok == Q4_OK) {
-    void *ptr = nullptr;
-    if (cudaGetSymbolAddress(&ptr, q4::g_status) != cudaSuccess) {
-      cudaGetLastError();
-      d.ok = Q4_ERR_CUDA;
-    }
-    d.status = reinterpret_cast<int *>(ptr);
-  }
-  cache[dev] = d;
-  filled[dev] = true;
-  return d;
-}
-
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 inline bool valid_bs(int b) { return b == 32 || b == 64 || b == 128 || b == 256; }
 inline bool valid_in_dtype(int d) { return d == Q4_F16 || d == Q4_BF16; }
@@ -163,38 +188,6 @@ size_t gemv_ws_for(const q4_state *s, int64_t *n_tiles, int64_t *n_stages) {
 size_t gemv_small_slots(int64_t total_stages, int64_t M) {
   const int64_t grid = std::min<int64_t>(total_stages, kGsMaxCtas);
   return align256((size_t)grid * 2 * kGsRows * (M <= 8 ? 8 : (M <= 16 ? 16 : 32)) * 4);
-}
-
-// ---- TMA descriptors ----------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-    cudaGetLastError();
-  });
-  return fn;
-}
-
-// 2-D row-major tensor [rows, cols] of `esize`-byte elements, box {bx, by}.
-bool make_map(CUtensorMap *m, CUtensorMapDataType dt, const void *base, int64_t rows, int64_t cols,
-              int esize, int bx, int by, CUtensorMapSwizzle sw) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)(cols * esize)};
-  const cuuint32_t box[2] = {(cuuint32_t)bx, (cuuint32_t)by};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The decode-batch path (M <= 16): the mma.sync kernel of gemv_small.cuh.

@@ -1,9 +1,11 @@
 // q4_internal.h -- host-side launcher entry points shared by the translation
 // units of libq4.so (not part of the public C ABI).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 #include <utility>
 
@@ -15,6 +17,19 @@
 #include "quantize_grouped.cuh"
 
 namespace q4 {
+// The current device as the compute calls see it (asked once per device).
+struct DeviceInfo {
+  int ok = Q4_ERR_NO_DEVICE;
+  int sms = 0;
+  int *status = nullptr;  // device address of q4::g_status
+};
+DeviceInfo device_info();
+extern std::atomic<uint64_t> g_wait_limit_ns;  // q4_set_wait_limit_ns
+extern std::atomic<int32_t> g_copy_stall;      // q4_set_copy_stall
+// Tensor map of a 2-D row-major tensor (stride_bytes 0: packed rows).
+bool make_map(CUtensorMap *m, CUtensorMapDataType dt, const void *base, int64_t rows, int64_t cols, int esize, int bx,
+              int by, CUtensorMapSwizzle sw, int64_t stride_bytes = 0);
+
 // Launch with programmatic stream serialization (the kernel calls
 // pdl_launch_then_wait() before any global memory access).
 template <typename... KArgs, typename... Args>

@@ -136,12 +136,13 @@ def linears_to_replace(module: torch.nn.Module, skip=("lm_head",)) -> list:
     return names
 
 
-def replace_linear(module: torch.nn.Module, skip=("lm_head",), **kw) -> torch.nn.Module:
+def replace_linear(module: torch.nn.Module, skip=("lm_head",), linear=Linear4bit, **kw) -> torch.nn.Module:
     """Swap the module's nn.Linear layers (except `skip`) for Linear4bit in
     place, quantizing each weight once; keyword arguments go to
-    Linear4bit.from_linear.  Returns the module."""
+    Linear4bit.from_linear.  linear=linear8bit.Linear8bit gives the 8-bit
+    integer layers instead.  Returns the module."""
     for name in linears_to_replace(module, skip):
         parent_name, _, child = name.rpartition(".")
         parent = module.get_submodule(parent_name) if parent_name else module
-        setattr(parent, child, Linear4bit.from_linear(getattr(parent, child), **kw))
+        setattr(parent, child, linear.from_linear(getattr(parent, child), **kw))
     return module

@@ -9,6 +9,7 @@ without a B200 every op raises Q4Error.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from dataclasses import dataclass
@@ -25,6 +26,7 @@ QTYPES = {"nf4": NF4, "int4_sym": INT4_SYM, "int4_asym": INT4_ASYM}
 _DT = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 _DT_INV = {v: k for k, v in _DT.items()}
 DQ_GROUP = 256
+INT8_MAX_K = 131071  # Q4_INT8_MAX_K
 
 
 class Q4Error(RuntimeError):
@@ -39,6 +41,12 @@ class _CState(ctypes.Structure):
                 ("packed", ctypes.c_void_p), ("absmax", ctypes.c_void_p), ("zero", ctypes.c_void_p),
                 ("absmax_q", ctypes.c_void_p), ("absmax_scale", ctypes.c_void_p),
                 ("absmax_mean", ctypes.c_void_p)]
+
+
+class _CKVCache(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("blocksize", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("pages", ctypes.c_int64), ("k_codes", ctypes.c_void_p),
+                ("k_state", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("v_state", ctypes.c_void_p)]
 
 
 _lib = None
@@ -79,6 +87,16 @@ def library():
             "q4_gemm": ([P, i32, i64, SP, P, i32, P, ctypes.c_size_t, P], i32),
             "q4_gemm_grouped": ([i32, ctypes.POINTER(P), ctypes.POINTER(SP), ctypes.POINTER(P), i64,
                                  i32, i32, P, ctypes.c_size_t, P], i32),
+            "q4_int8_quantize_rows": ([P, i32, i64, i64, i64, P, i64, P, P], i32),
+            "q4_int8_gemm_workspace_size": ([i64, i64, i64, ctypes.POINTER(sz)], i32),
+            "q4_int8_gemm": ([P, i64, P, i64, P, i64, P, i64, i64, P, i32, P, i64, i32, P, sz, P], i32),
+            "q4_int8_linear_workspace_size": ([i64, i64, i64, ctypes.POINTER(sz)], i32),
+            "q4_int8_linear": ([P, i32, i64, i64, P, i64, P, i64, i64, P, i32, P, i64, i32, P, sz, P], i32),
+            "q4_kv_append": ([ctypes.POINTER(_CKVCache), P, P, i32, i64, i64, i64, i64, i64, P, P], i32),
+            "q4_kv_dequantize": ([ctypes.POINTER(_CKVCache), P, i64, P, P, i32, P], i32),
+            "q4_kv_attention_workspace_size": ([ctypes.POINTER(_CKVCache), i64, i64, i32, ctypes.POINTER(sz)], i32),
+            "q4_kv_attention": ([ctypes.POINTER(_CKVCache), P, i32, i64, i32, i64, i64, P, P, P, i64, i64, i64, i64,
+                                 ctypes.c_float, i32, i64, P, P, P, sz, P], i32),
             "q4_device_status": ([ctypes.POINTER(i32)], i32),
             "q4_clear_device_status": ([], i32),
             "q4_set_wait_limit_ns": ([ctypes.c_uint64], i32),
@@ -478,3 +496,377 @@ def gemm_grouped(As, states, out_dtype: torch.dtype | None = None, outs=None, st
 def gemm(A: torch.Tensor, st: Q4State, out_dtype: torch.dtype | None = None, out=None,
          stream=None) -> torch.Tensor:
     return gemm_grouped([A], [st], out_dtype, None if out is None else [out], stream)[0]
+
+
+# ------------------------------------------- 8-bit integers and the KV cache --
+# These calls run on the device and the current stream of their tensors'
+# device (or on `stream`); what they allocate belongs to that stream.  Their
+# workspaces are one per device, kind and stream; a call that is captured into
+# a CUDA graph takes a workspace of its own, so graphs share none.
+
+class _On:
+    """Makes a tensor's device current, and `stream` when given, for a call."""
+    __slots__ = ("dev", "ctx")
+
+    def __init__(self, t: torch.Tensor, stream):
+        if not t.is_cuda:
+            raise Q4Error("no CUDA device: libq4 has no CPU fallback" if not torch.cuda.is_available()
+                          else "tensor must be on a CUDA device")
+        self.ctx = None
+        if stream is not None:
+            if stream.device != t.device:
+                raise Q4Error(f"stream is on {stream.device}, the tensors on {t.device}")
+            self.ctx = torch.cuda.stream(stream)
+        elif t.device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *a):
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
+
+
+def _stream_workspace(device, kind: str, stream: int, nbytes: int) -> torch.Tensor | None:
+    """A zero-filled workspace for the current stream."""
+    if nbytes == 0:
+        return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    key = (device.index, kind, stream)
+    t = _ws.get(key)
+    if t is None or t.numel() < nbytes:
+        t = _ws[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    return t
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise Q4Error(f"{name} is on {t.device}, expected {dev}")
+
+
+def _rows16(x: torch.Tensor, name: str) -> torch.Tensor:
+    if x.dtype not in (torch.float16, torch.bfloat16):
+        raise Q4Error(f"{name} must be float16 or bfloat16, got {x.dtype}")
+    return x
+
+
+def int8_quantize_rows(X: torch.Tensor, stream=None) -> tuple:
+    """(codes, scale) of a 2-D fp16/bf16 tensor: symmetric 8-bit codes with one
+    scale per row, X ~ codes * scale[:, None].  For a weight [N, K] (a scale
+    per output channel, once at load time) or for activations [M, K] (a scale
+    per token).  The code rows are padded to a multiple of 16 bytes: codes is
+    a [rows, K] view of that buffer."""
+    _rows16(X, "X")
+    if X.dim() != 2:
+        raise Q4Error("X must be 2-D")
+    rows, K = X.shape
+    if K < 1:
+        raise Q4Error("X has no columns")
+    if X.stride(1) != 1 and K > 1 or rows > 1 and X.stride(0) < K:
+        X = X.contiguous()
+    with _On(X, stream) as s:
+        ldc = (K + 15) // 16 * 16
+        codes = torch.empty(rows, ldc, dtype=torch.int8, device=X.device)[:, :K]
+        scale = torch.empty(rows, dtype=torch.float32, device=X.device)
+        if rows:
+            _check(library().q4_int8_quantize_rows(X.data_ptr(), _DT[X.dtype], rows, K, max(X.stride(0), K),
+                                                   codes.data_ptr(), ldc, scale.data_ptr(), s),
+                   "q4_int8_quantize_rows")
+    return codes, scale
+
+
+def _check_codes(name, codes, scale):
+    if codes.dtype != torch.int8 or codes.dim() != 2 or scale.dtype != torch.float32 or scale.dim() != 1:
+        raise Q4Error(f"{name} must be int8 [rows, K] codes with float32 [rows] scales")
+    if scale.shape[0] != codes.shape[0] or not scale.is_contiguous():
+        raise Q4Error(f"{name}: one contiguous scale per row is needed")
+    if codes.stride(1) != 1 or codes.stride(0) % 16 or codes.data_ptr() % 16:
+        raise Q4Error(f"{name}: code rows must be adjacent bytes that begin at multiples of 16 bytes "
+                      "(as int8_quantize_rows gives them)")
+
+
+def _check_bias_out(bias, out, M, N, out_dtype, dev):
+    if bias is not None and (bias.shape != (N,) or bias.dtype not in _DT or not bias.is_contiguous()):
+        raise Q4Error(f"bias must be a contiguous float tensor of {N} elements")
+    if out is None:
+        return torch.empty(M, N, dtype=out_dtype, device=dev)
+    if out.shape != (M, N) or out.dtype != out_dtype or out.stride(1) != 1 or out.stride(0) < N:
+        raise Q4Error(f"out must be {out_dtype} [{M}, {N}] with adjacent elements")
+    return out
+
+
+_int8_ws_need = {}  # (M, N, K) -> workspace bytes of the product and of the linear layer
+
+
+def _int8_ws_sizes(M, N, K):
+    key = (M, N, K)
+    need = _int8_ws_need.get(key)
+    if need is None:
+        a, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+        _check(library().q4_int8_gemm_workspace_size(M, N, K, ctypes.byref(a)), "q4_int8_gemm_workspace_size")
+        _check(library().q4_int8_linear_workspace_size(M, N, K, ctypes.byref(b)), "q4_int8_linear_workspace_size")
+        if len(_int8_ws_need) >= 4096:
+            _int8_ws_need.clear()
+        need = _int8_ws_need[key] = (a.value, b.value)
+    return need
+
+
+def int8_gemm(A: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor,
+              bias: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float16, out=None,
+              stream=None) -> torch.Tensor:
+    """Y = (A . W^T) * a_scale[:, None] * w_scale[None, :] + bias from 8-bit
+    codes A [M, K] and W [N, K] (see int8_quantize_rows): exact 32-bit integer
+    sums, one rounding to out_dtype (fp16, bf16 or fp32)."""
+    _check_codes("A", A, a_scale)
+    _check_codes("W", W, w_scale)
+    (M, K), N = A.shape, W.shape[0]
+    if W.shape[1] != K:
+        raise Q4Error(f"A has {K} columns, W {W.shape[1]}")
+    if out_dtype not in _DT:
+        raise Q4Error(f"out_dtype {out_dtype} is not float16, bfloat16 or float32")
+    _same_device(A.device, a_scale=a_scale, W=W, w_scale=w_scale, bias=bias, out=out)
+    with _On(A, stream) as s:
+        y = _check_bias_out(bias, out, M, N, out_dtype, A.device)
+        if M and N:
+            ws = _stream_workspace(A.device, "int8", s, _int8_ws_sizes(M, N, K)[0])
+            _check(library().q4_int8_gemm(
+                A.data_ptr(), A.stride(0), a_scale.data_ptr(), M, W.data_ptr(), W.stride(0), w_scale.data_ptr(), N, K,
+                None if bias is None else bias.data_ptr(), 0 if bias is None else _DT[bias.dtype], y.data_ptr(),
+                max(y.stride(0), N), _DT[out_dtype], None if ws is None else ws.data_ptr(),
+                0 if ws is None else ws.numel(), s), "q4_int8_gemm")
+    return y
+
+
+def int8_linear(X: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, bias: torch.Tensor | None = None,
+                out_dtype: torch.dtype | None = None, out=None, stream=None) -> torch.Tensor:
+    """Y = X . W^T + bias with 16-bit activations X [M, K], quantized per token
+    on the way, and 8-bit weights (see int8_quantize_rows): int8_gemm of
+    int8_quantize_rows(X), in one call."""
+    _rows16(X, "X")
+    _check_codes("W", W, w_scale)
+    if X.dim() != 2 or X.shape[1] != W.shape[1]:
+        raise Q4Error(f"X must be [M, {W.shape[1]}], got {tuple(X.shape)}")
+    (M, K), N = X.shape, W.shape[0]
+    out_dtype = out_dtype or X.dtype
+    if out_dtype not in _DT:
+        raise Q4Error(f"out_dtype {out_dtype} is not float16, bfloat16 or float32")
+    _same_device(X.device, W=W, w_scale=w_scale, bias=bias, out=out)
+    if X.stride(1) != 1 and K > 1 or M > 1 and X.stride(0) < K:
+        X = X.contiguous()
+    with _On(X, stream) as s:
+        y = _check_bias_out(bias, out, M, N, out_dtype, X.device)
+        if M and N:
+            ws = _stream_workspace(X.device, "int8", s, _int8_ws_sizes(M, N, K)[1])
+            _check(library().q4_int8_linear(
+                X.data_ptr(), _DT[X.dtype], max(X.stride(0), K), M, W.data_ptr(), W.stride(0), w_scale.data_ptr(), N,
+                K, None if bias is None else bias.data_ptr(), 0 if bias is None else _DT[bias.dtype], y.data_ptr(),
+                max(y.stride(0), N), _DT[out_dtype], ws.data_ptr(), ws.numel(), s), "q4_int8_linear")
+    return y
+
+
+@dataclass
+class KVCache:
+    """A paged key/value cache in 4 bits (its four device buffers; the format
+    is that of q4_kv_cache in include/q4.h).  codes: uint8 [pages, kv_heads,
+    page_size, head_dim / 2]; state: float16 [pages, kv_heads, page_size,
+    head_dim / blocksize, 2], the pairs (scale, zero-point)."""
+    k_codes: torch.Tensor
+    k_state: torch.Tensor
+    v_codes: torch.Tensor
+    v_state: torch.Tensor
+
+    def __post_init__(self):
+        c, st = self.k_codes, self.k_state
+        if c.dim() != 4 or st.dim() != 5 or st.shape[-1] != 2 or st.shape[:3] != c.shape[:3] or not st.shape[3] \
+                or 2 * c.shape[3] % st.shape[3]:
+            raise Q4Error("codes must be [pages, heads, page_size, head_dim / 2], states [pages, heads, page_size, "
+                          "head_dim / blocksize, 2]")
+        for name, t, want in (("k_codes", c, torch.uint8), ("v_codes", self.v_codes, torch.uint8),
+                              ("k_state", st, torch.float16), ("v_state", self.v_state, torch.float16)):
+            if t.dtype != want or not t.is_contiguous() or t.device != c.device or \
+                    t.shape != (c if want == torch.uint8 else st).shape:
+                raise Q4Error(f"{name} must be a contiguous {want} tensor like its partners")
+        s = _CKVCache()
+        s.head_dim, s.blocksize = self.head_dim, self.blocksize
+        s.kv_heads, s.page_size, s.pages = self.kv_heads, self.page_size, self.pages
+        s.k_codes, s.k_state = c.data_ptr(), st.data_ptr()
+        s.v_codes, s.v_state = self.v_codes.data_ptr(), self.v_state.data_ptr()
+        self._c = s
+        self._ref = ctypes.byref(s)
+        self._ws_need = {}  # (batch, rows, query heads) -> workspace bytes of attention
+
+    def __setattr__(self, name, value):
+        if name in ("k_codes", "k_state", "v_codes", "v_state") and "_c" in self.__dict__:
+            raise Q4Error("the buffers of a KVCache are fixed: make a new one")
+        object.__setattr__(self, name, value)
+
+    @property
+    def pages(self) -> int:
+        return self.k_codes.shape[0]
+
+    @property
+    def kv_heads(self) -> int:
+        return self.k_codes.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.k_codes.shape[2]
+
+    @property
+    def head_dim(self) -> int:
+        return 2 * self.k_codes.shape[3]
+
+    @property
+    def blocksize(self) -> int:
+        return self.head_dim // self.k_state.shape[3]
+
+    @property
+    def device(self):
+        return self.k_codes.device
+
+    def held_bytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.k_codes, self.k_state, self.v_codes, self.v_state))
+
+
+def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, blocksize: int = 64,
+             device="cuda") -> KVCache:
+    """Allocate a cache of pages * page_size tokens (head_dim 64 or 128;
+    blocksize 64 or 128, a divisor of it; page_size 16, 32, 64, 128 or 256)."""
+    if head_dim not in (64, 128) or blocksize not in (64, 128) or head_dim % blocksize:
+        raise Q4Error(f"head_dim {head_dim} with blocksize {blocksize}: head_dim must be 64 or 128, blocksize 64 or 128 "
+                      "and a divisor of it")
+    if page_size not in (16, 32, 64, 128, 256):
+        raise Q4Error(f"page_size {page_size} is not 16, 32, 64, 128 or 256")
+    if pages < 1 or kv_heads < 1:
+        raise Q4Error("a cache needs at least one page and one head")
+    c = torch.empty(2, pages, kv_heads, page_size, head_dim // 2, dtype=torch.uint8, device=device)
+    s = torch.empty(2, pages, kv_heads, page_size, head_dim // blocksize, 2, dtype=torch.float16, device=device)
+    return KVCache(c[0], s[0], c[1], s[1])
+
+
+def _head_rows(x: torch.Tensor, heads, dim: int, name: str) -> torch.Tensor:
+    """x as [rows, heads, dim] with strides the kernels read (a copy if its own are not)."""
+    _rows16(x, name)
+    if x.dim() != 3 or x.shape[2] != dim or (heads is not None and x.shape[1] != heads):
+        raise Q4Error(f"{name} must be [rows, {heads or 'heads'}, {dim}], got {tuple(x.shape)}")
+    if x.stride(2) != 1 or x.stride(0) % 8 or x.stride(1) % 8 or x.data_ptr() % 16 or x.stride(0) < 0:
+        x = x.contiguous()
+        if x.data_ptr() % 16:
+            x = x.clone()
+    return x
+
+
+def _index(t: torch.Tensor, dtype, shape, name: str) -> torch.Tensor:
+    if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and t.shape[i] != w for i, w in enumerate(shape)):
+        raise Q4Error(f"{name} must be {dtype} of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        t = t.contiguous()
+    return t
+
+
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+    """Quantize keys and values [tokens, kv_heads, head_dim] (fp16 or bf16) into
+    the cache at slots (int64 [tokens], page * page_size + offset; a negative
+    one passes its token over).  The slots of a call are distinct."""
+    with _On(k, stream) as s:
+        k = _head_rows(k, cache.kv_heads, cache.head_dim, "k")
+        v = _head_rows(v, cache.kv_heads, cache.head_dim, "v")
+        if k.shape != v.shape or k.dtype != v.dtype:
+            raise Q4Error("k and v must have one shape and dtype")
+        slots = _index(slots, torch.int64, (k.shape[0],), "slots")
+        _same_device(k.device, v=v, slots=slots, cache=cache)
+        if k.shape[0]:
+            _check(library().q4_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), _DT[k.dtype], k.shape[0],
+                                          k.stride(0), k.stride(1), v.stride(0), v.stride(1), slots.data_ptr(), s),
+                   "q4_kv_append")
+
+
+def kv_dequantize(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.float16, stream=None) -> tuple:
+    """(k, v) [n, kv_heads, head_dim] of the given slots as 16-bit floats;
+    zeros for a negative slot."""
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise Q4Error("dtype must be float16 or bfloat16")
+    with _On(slots, stream) as s:
+        slots = _index(slots, torch.int64, (None,), "slots")
+        _same_device(slots.device, cache=cache)
+        n = slots.shape[0]
+        k = torch.empty(n, cache.kv_heads, cache.head_dim, dtype=dtype, device=slots.device)
+        v = torch.empty_like(k)
+        if n:
+            _check(library().q4_kv_dequantize(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _DT[dtype],
+                                              s), "q4_kv_dequantize")
+    return k, v
+
+
+def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 cu_seqlens_q: torch.Tensor | None = None, max_q: int | None = None, scale: float | None = None,
+                 causal: bool = True, window: int = 0, out: torch.Tensor | None = None, return_lse: bool = False,
+                 stream=None):
+    """softmax(scale q k^T) v over the cached keys and values.
+
+    q [rows, q_heads, head_dim] (fp16 or bf16; q_heads a multiple of the
+    cache's heads); block_table int32 [batch, n], the page of each page_size
+    keys; seq_lens int32 [batch], keys of each sequence, those of its query
+    rows included.  cu_seqlens_q int32 [batch + 1]: sequence b has the rows
+    cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1, its last ones; None: one row
+    each (rows = batch).  max_q: the most rows of a sequence, a hint (default:
+    rows of the whole call when cu_seqlens_q is given).  scale: 1 /
+    sqrt(head_dim) unless given.  causal: a row attends to the keys up to its
+    own position; window > 0: only to the last `window` of them.  Rows that
+    attend to nothing are zero, with log sum exp -inf; rows outside
+    cu_seqlens_q are left as they were (pass `out` to have them defined).
+    Returns out [rows, q_heads, head_dim], with return_lse also float32 [rows,
+    q_heads]."""
+    with _On(q, stream) as s:
+        dim = cache.head_dim
+        q = _head_rows(q, None, dim, "q")
+        rows, heads, _ = q.shape
+        if heads == 0 or heads % cache.kv_heads:
+            raise Q4Error(f"{heads} query heads are no multiple of {cache.kv_heads} key/value heads")
+        if window < 0:
+            raise Q4Error("window must be 0 (none) or positive")
+        seq_lens = _index(seq_lens, torch.int32, (None,), "seq_lens")
+        batch = seq_lens.shape[0]
+        if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch or \
+                block_table.shape[1] < 1:
+            raise Q4Error(f"block_table must be int32 [{batch}, pages], got {block_table.dtype} "
+                          f"{tuple(block_table.shape)}")
+        if block_table.stride(1) != 1 or block_table.stride(0) < block_table.shape[1]:
+            block_table = block_table.contiguous()
+        if cu_seqlens_q is not None:
+            cu_seqlens_q = _index(cu_seqlens_q, torch.int32, (batch + 1,), "cu_seqlens_q")
+        elif rows != batch:
+            raise Q4Error(f"{rows} query rows for {batch} sequences: pass cu_seqlens_q")
+        _same_device(q.device, cache=cache, block_table=block_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q,
+                     out=out)
+        if out is None:
+            out = torch.empty(rows, heads, dim, dtype=q.dtype, device=q.device)
+        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+            raise Q4Error("out must be a contiguous tensor of q's shape and dtype")
+        lse = torch.empty(rows, heads, dtype=torch.float32, device=q.device) if return_lse else None
+        if rows and batch:
+            key = (batch, rows, heads)
+            need = cache._ws_need.get(key)
+            if need is None:
+                n = ctypes.c_size_t(0)
+                _check(library().q4_kv_attention_workspace_size(cache._ref, batch, rows, heads, ctypes.byref(n)),
+                       "q4_kv_attention_workspace_size")
+                if len(cache._ws_need) >= 4096:
+                    cache._ws_need.clear()
+                need = cache._ws_need[key] = n.value
+            ws = _stream_workspace(q.device, "kv", s, need)
+            if max_q is None:
+                max_q = 1 if cu_seqlens_q is None else rows
+            _check(library().q4_kv_attention(
+                cache._ref, q.data_ptr(), _DT[q.dtype], rows, heads, q.stride(0), q.stride(1),
+                None if cu_seqlens_q is None else cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
+                block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]), block_table.shape[1], batch,
+                max(1, max_q), 1.0 / math.sqrt(dim) if scale is None else scale, int(causal), window, out.data_ptr(),
+                None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
+                0 if ws is None else ws.numel(), s), "q4_kv_attention")
+    return (out, lse) if return_lse else out

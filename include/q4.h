@@ -70,6 +70,7 @@ extern "C" {
 #define Q4_STATUS_NONFINITE 1  /* quantize met a block with a non-finite absmax */
 #define Q4_STATUS_TIMEOUT 2    /* a bounded device-side wait gave up */
 #define Q4_STATUS_LAYOUT 4     /* a kernel found too little shared memory and computed nothing */
+#define Q4_STATUS_INDEX 8      /* a slot, page, length or row range outside its cache or table was passed over */
 
 /* ---- enums ------------------------------------------------------------- */
 typedef enum {
@@ -331,6 +332,141 @@ Q4_API int q4_gemm(const void *A, int32_t a_dtype, int64_t M, const q4_state *Wq
 Q4_API int q4_gemm_grouped(int32_t count, const void *const *A, const q4_state *const *Wq,
                     void *const *Y, int64_t M, int32_t a_dtype, int32_t y_dtype, void *workspace,
                     size_t workspace_bytes, void *stream);
+
+/* ---- 8-bit integer linear layer (W8A8) --------------------------------- */
+
+/*
+ * q4_int8_quantize_rows -- symmetric 8-bit codes with one scale per row: of a
+ * weight [N, K] (a scale per output channel) at load time, or of activations
+ * [M, K] (a scale per token).
+ *   s = max|x| / 127, q = rint(x / s) (IEEE binary32, correctly rounded
+ *   division, ties to even); an all-zero row has s = 0 and codes 0.  A row
+ *   with an infinity or a NaN gets s = NaN and codes 0 and sets
+ *   Q4_STATUS_NONFINITE, so that every product with it is NaN.
+ *   X      device, rows x cols 16-bit floats of x_dtype, rows `ldx` elements
+ *          apart (any alignment of 2 bytes; rows at 16 bytes are read faster).
+ *   codes  device, int8, rows `ldc` bytes apart; 16-byte aligned, ldc a
+ *          multiple of 16 and >= cols.  Bytes past cols are left as they were.
+ *   scale  device, float [rows].
+ * Q4_ERR_SHAPE for rows < 1, cols < 1, cols > Q4_INT8_MAX_K or a short stride.
+ */
+#define Q4_INT8_MAX_K 131071 /* K 128^2 < 2^31: no int8 operands overflow the 32-bit sums */
+Q4_API int q4_int8_quantize_rows(const void *X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                 int8_t *codes, int64_t ldc, float *scale, void *stream);
+
+/*
+ * q4_int8_gemm -- Y[M, N] = a_scale[m] w_scale[n] sum_k A[m, k] W[n, k] + bias[n]:
+ * the sum in 32-bit integers (exact), then binary32 with one rounding to
+ * y_dtype, for any M, N >= 1 and 1 <= K <= Q4_INT8_MAX_K.
+ *   A, W   device, int8, 16-byte aligned, rows lda / ldw bytes apart
+ *          (multiples of 16, >= K); what lies past K is not read into a sum.
+ *   bias   device, [N] of bias_dtype (Q4_F16 / Q4_BF16 / Q4_F32), or NULL.
+ *   Y      device, y_dtype (Q4_F16 / Q4_BF16 / Q4_F32), rows ldy elements apart
+ *          (>= N); what lies past N is left as it was.
+ *   workspace  device, 16-byte aligned, q4_int8_gemm_workspace_size() bytes,
+ *          zero-filled before its first use; every call leaves it zero-filled.
+ *          Calls that run at once need workspaces of their own.
+ */
+Q4_API int q4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes);
+Q4_API int q4_int8_gemm(const int8_t *A, int64_t lda, const float *a_scale, int64_t M, const int8_t *W, int64_t ldw,
+                        const float *w_scale, int64_t N, int64_t K, const void *bias, int32_t bias_dtype, void *Y,
+                        int64_t ldy, int32_t y_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The linear layer on 16-bit activations X [M, K] (rows ldx elements apart):
+ * q4_int8_quantize_rows into the workspace, then q4_int8_gemm; bit for bit
+ * their results.  workspace: q4_int8_linear_workspace_size() bytes, with the
+ * rules of q4_int8_gemm (its head is the GEMM's workspace, the codes and
+ * scales of X follow and need no zero-fill). */
+Q4_API int q4_int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes);
+Q4_API int q4_int8_linear(const void *X, int32_t x_dtype, int64_t ldx, int64_t M, const int8_t *W, int64_t ldw,
+                          const float *w_scale, int64_t N, int64_t K, const void *bias, int32_t bias_dtype, void *Y,
+                          int64_t ldy, int32_t y_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- key/value cache in 4 bits, and attention over it ------------------- */
+
+/*
+ * A paged cache of keys and values.  The caller owns the four buffers:
+ *   k_codes, v_codes  uint8 [pages][kv_heads][page_size][head_dim / 2]
+ *   k_state, v_state  [pages][kv_heads][page_size][head_dim / blocksize] pairs
+ *                     (s, z) of binary16, 4 bytes each
+ * Each token's vector of a head is cut into blocks of `blocksize` elements,
+ * quantized by the rule of Q4_INT4_ASYM | Q4_SCALE_F16 (bit for bit the codes,
+ * scale and zero-point that q4_quantize gives the block): x^ = s (q - z).
+ * Within a vector the codes stand in words of 8 (low nibble first), the
+ * words of its blocks interleaved: word i * (head_dim / blocksize) + j holds
+ * elements 8 i .. 8 i + 7 of block j.
+ * head_dim 64 or 128; blocksize 64 or 128 and a divisor of head_dim;
+ * page_size 16, 32, 64, 128 or 256; all four buffers 16-byte aligned.
+ * A token's place is its slot, page * page_size + offset.  Places that no
+ * call has written may hold anything: nothing is read past a sequence's
+ * length into a result.
+ */
+typedef struct {
+  int32_t head_dim, blocksize, kv_heads, page_size;
+  int64_t pages;
+  uint8_t *k_codes;
+  void *k_state;
+  uint8_t *v_codes;
+  void *v_state;
+} q4_kv_cache;
+
+/*
+ * q4_kv_append -- quantize `tokens` key and value vectors into the cache.
+ *   K, V   device, 16-bit floats of `dtype`, [tokens][kv_heads][head_dim] with
+ *          the given strides in elements (token and head strides multiples of
+ *          8, the elements of a vector adjacent), 16-byte aligned.
+ *   slots  device, int64 [tokens].  A negative slot passes its token over (a
+ *          padded batch); one past the cache does too and sets
+ *          Q4_STATUS_INDEX.  The slots of a call are distinct: of a slot given
+ *          twice the cache holds either token's blocks, whole or mixed.
+ * A block with an infinity or a NaN, or whose range max(x, 0) - min(x, 0)
+ * exceeds 61440 (its values would leave binary16), is stored with s = NaN and
+ * sets Q4_STATUS_NONFINITE: rows that attend to it give NaN.
+ */
+Q4_API int q4_kv_append(const q4_kv_cache *cache, const void *K, const void *V, int32_t dtype, int64_t tokens,
+                        int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                        int64_t v_head_stride, const int64_t *slots, void *stream);
+
+/* The cached vectors of n slots as 16-bit floats, K and V [n][kv_heads]
+ * [head_dim] packed (16-byte aligned): x^ = s (q - z) rounded once to `dtype`.
+ * Zeros for a negative slot, and with Q4_STATUS_INDEX for one past the cache. */
+Q4_API int q4_kv_dequantize(const q4_kv_cache *cache, const int64_t *slots, int64_t n, void *K, void *V,
+                            int32_t dtype, void *stream);
+
+/*
+ * q4_kv_attention -- softmax(scale Q K^T) V over the cache, for single tokens,
+ * a few (drafted) tokens, and prompts.
+ *   Q      device, 16-bit floats of `dtype`, [total_q][q_heads][head_dim] with
+ *          the given strides in elements (multiples of 8), 16-byte aligned;
+ *          q_heads a multiple of kv_heads, query head h reads kv head
+ *          h / (q_heads / kv_heads).
+ *   cu_q   device, int32 [batch + 1], ascending: sequence b has the query rows
+ *          cu_q[b] .. cu_q[b + 1] - 1; rows outside are left as they were.
+ *          NULL: one row for each sequence (total_q = batch).
+ *   lens   device, int32 [batch]: keys of each sequence, its query rows' own
+ *          included (append first); 0 is allowed.
+ *   table  device, int32 [batch][table_stride], its first table_pages columns
+ *          valid: page of each page_size keys.  Entries past a length are not
+ *          read.
+ * Row i of n stands at position p = len - n + i and attends to the keys
+ * j <= p (causal 1) or to all (causal 0), and with window w > 0 only to
+ * j > p - w.  A row that attends to nothing gives zeros and lse -inf.
+ *   out    device, [total_q][q_heads][head_dim] packed, of `dtype`.
+ *   lse    device, float [total_q][q_heads], log sum exp of the scaled
+ *          scores, or NULL.
+ *   max_q  the most rows of any sequence: it only helps to choose the kernel.
+ *   workspace  as q4_int8_gemm's, q4_kv_attention_workspace_size() bytes.
+ * Entries outside the cache, lengths outside the table and row ranges outside
+ * Q are cut off and set Q4_STATUS_INDEX.  The order of every sum is fixed by
+ * the arguments and the device: identical calls give identical bits.
+ */
+Q4_API int q4_kv_attention_workspace_size(const q4_kv_cache *cache, int64_t batch, int64_t total_q, int32_t q_heads,
+                                          size_t *bytes);
+Q4_API int q4_kv_attention(const q4_kv_cache *cache, const void *Q, int32_t dtype, int64_t total_q, int32_t q_heads,
+                           int64_t q_token_stride, int64_t q_head_stride, const int32_t *cu_q, const int32_t *lens,
+                           const int32_t *table, int64_t table_stride, int64_t table_pages, int64_t batch,
+                           int64_t max_q, float scale, int32_t causal, int64_t window, void *out, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---- status and introspection ----------------------------------------- */
 
