@@ -1,7 +1,6 @@
 // k_kv.cu -- launchers of the 4-bit key/value cache kernels.
 #include "q4_internal.h"
-#include "kv_attention.cuh"
-#include "kv_cache.cuh"
+#include "serve_internal.h"
 
 namespace q4 {
 namespace {

@@ -6,17 +6,7 @@
 #include <algorithm>
 
 #include "q4_internal.h"
-#include "int8_gemm.cuh"
-#include "int8_quantize.cuh"
-#include "kv_attention.cuh"
-
-namespace q4 {
-int run_int8_quantize(int dt, const I8QuantParams &p, cudaStream_t st);
-int run_int8_gemm(const I8GemmParams &p, cudaStream_t st);
-int run_kv_append(int dt, int D, int B, const KvAppendParams &p, cudaStream_t st);
-int run_kv_dequantize(int dt, int D, int B, const KvDequantParams &p, cudaStream_t st);
-int run_kv_attention(int dt, int D, int B, const KvAttnParams &p, cudaStream_t st);
-}  // namespace q4
+#include "serve_internal.h"
 
 using namespace q4;
 
@@ -26,6 +16,11 @@ inline bool in16(int d) { return d == Q4_F16 || d == Q4_BF16; }
 inline bool any_float(int d) { return d == Q4_F16 || d == Q4_BF16 || d == Q4_F32; }
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 constexpr int64_t kMaxRows = INT32_MAX;
+constexpr int kDefaultSms = 148;  // sizes asked for without a device are those of a B200
+int plan_sms() {
+  const DeviceInfo di = device_info();
+  return di.ok == Q4_OK ? di.sms : kDefaultSms;
+}
 
 int check_linear(int64_t M, int64_t N, int64_t K) {
   if (M < 1 || N < 1 || K < 1 || M > kMaxRows || N > kMaxRows || K > Q4_INT8_MAX_K) return Q4_ERR_SHAPE;
@@ -73,7 +68,9 @@ int q4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes) 
   if (!bytes) return Q4_ERR_ARG;
   const int rc = check_linear(M, N, K);
   if (rc != Q4_OK) return rc;
-  *bytes = 0;
+  const I8Plan pl = int8_plan(M, N, K, plan_sms());
+  if (!pl.nt) return Q4_ERR_SHAPE;
+  *bytes = pl.ws_bytes;
   return Q4_OK;
 }
 
@@ -81,52 +78,62 @@ int q4_int8_gemm(const int8_t *A, int64_t lda, const float *a_scale, int64_t M, 
                  const float *w_scale, int64_t N, int64_t K, const void *bias, int32_t bias_dtype, void *Y, int64_t ldy,
                  int32_t y_dtype, void *workspace, size_t workspace_bytes, void *stream) {
   if (!A || !a_scale || !W || !w_scale || !Y || !any_float(y_dtype) || (bias && !any_float(bias_dtype))) return Q4_ERR_ARG;
-  size_t need = 0;
-  const int rc = q4_int8_gemm_workspace_size(M, N, K, &need);
+  int rc = check_linear(M, N, K);
   if (rc != Q4_OK) return rc;
   if (lda < K || ldw < K || ldy < N || lda % 16 || ldw % 16) return Q4_ERR_SHAPE;
-  if (!aligned16(A) || !aligned16(W)) return Q4_ERR_ALIGN;
-  if (need && (!workspace || workspace_bytes < need)) return Q4_ERR_WORKSPACE;
+  if (!aligned16(A) || !aligned16(W) || !aligned16(workspace)) return Q4_ERR_ALIGN;
   const DeviceInfo di = device_info();
+  const I8Plan pl = int8_plan(M, N, K, di.ok == Q4_OK ? di.sms : kDefaultSms);
+  if (!pl.nt) return Q4_ERR_SHAPE;
+  if (pl.ws_bytes && (!workspace || workspace_bytes < pl.ws_bytes)) return Q4_ERR_WORKSPACE;
   if (di.ok != Q4_OK) return di.ok;
-  I8GemmParams p;
-  p.A = A, p.W = W, p.lda = lda, p.ldw = ldw, p.ldy = ldy;
+  static thread_local I8GemmParams p;
+  memset(&p, 0, sizeof(p));
   p.sa = a_scale, p.sw = w_scale;
   p.bias = bias, p.bias_dtype = bias_dtype;
-  p.Y = Y, p.y_dtype = y_dtype;
-  p.M = M, p.N = N, p.K = K;
+  p.Y = Y, p.y_dtype = y_dtype, p.ldy = ldy;
+  p.M = (int32_t)M, p.N = (int32_t)N;
+  p.nk = (int32_t)((K + kI8Bk - 1) / kI8Bk);
+  p.tiles_t = pl.tiles_t, p.tiles_n = pl.tiles_n;
+  p.whole = pl.whole, p.cut_ctas = pl.cut_ctas;
+  p.prefetch = M <= 64 ? 16 : 4;
+  p.counts = (unsigned *)workspace;
+  p.sums = (int32_t *)((char *)workspace + pl.count_bytes);
+  p.stall_copies = g_copy_stall.load(std::memory_order_relaxed);
+  p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   p.status = di.status;
-  return run_int8_gemm(p, (cudaStream_t)stream);
+  const I8Operands o = {A, W, lda, ldw, M, N, K};
+  return run_int8_gemm(o, pl, p, (cudaStream_t)stream);
 }
 
-int q4_int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes) {
-  size_t head = 0;
-  const int rc = q4_int8_gemm_workspace_size(M, N, K, &head);
-  if (rc != Q4_OK) return rc;
+int q4_int8_linear_scratch_size(int64_t M, int64_t K, size_t *bytes) {
   if (!bytes) return Q4_ERR_ARG;
-  *bytes = up256(head) + up256((size_t)M * 4) + (size_t)M * ((size_t)(K + 15) / 16 * 16);
+  const int rc = check_linear(M, 1, K);
+  if (rc != Q4_OK) return rc;
+  *bytes = up256((size_t)M * 4) + (size_t)M * ((size_t)(K + 15) / 16 * 16);
   return Q4_OK;
 }
 
 int q4_int8_linear(const void *X, int32_t x_dtype, int64_t ldx, int64_t M, const int8_t *W, int64_t ldw,
                    const float *w_scale, int64_t N, int64_t K, const void *bias, int32_t bias_dtype, void *Y, int64_t ldy,
-                   int32_t y_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+                   int32_t y_dtype, void *scratch, size_t scratch_bytes, void *workspace, size_t workspace_bytes,
+                   void *stream) {
   if (!X || !W || !w_scale || !Y || !in16(x_dtype) || !any_float(y_dtype) || (bias && !any_float(bias_dtype)))
     return Q4_ERR_ARG;
   size_t head = 0, need = 0;
   int rc = q4_int8_gemm_workspace_size(M, N, K, &head);
-  if (rc == Q4_OK) rc = q4_int8_linear_workspace_size(M, N, K, &need);
+  if (rc == Q4_OK) rc = q4_int8_linear_scratch_size(M, K, &need);
   if (rc != Q4_OK) return rc;
   if (ldx < K || ldw < K || ldw % 16 || ldy < N) return Q4_ERR_SHAPE;
-  if (!aligned16(W) || !aligned16(workspace)) return Q4_ERR_ALIGN;
-  if (!workspace || workspace_bytes < need) return Q4_ERR_WORKSPACE;
+  if (!aligned16(W) || !aligned16(workspace) || !aligned16(scratch)) return Q4_ERR_ALIGN;
+  if (!scratch || scratch_bytes < need || (head && (!workspace || workspace_bytes < head))) return Q4_ERR_WORKSPACE;
   const int64_t ldc = (K + 15) / 16 * 16;
-  float *scale = (float *)((char *)workspace + up256(head));
-  int8_t *codes = (int8_t *)workspace + up256(head) + up256((size_t)M * 4);
+  float *scale = (float *)scratch;
+  int8_t *codes = (int8_t *)scratch + up256((size_t)M * 4);
   rc = q4_int8_quantize_rows(X, x_dtype, M, K, ldx, codes, ldc, scale, stream);
   if (rc != Q4_OK) return rc;
-  return q4_int8_gemm(codes, ldc, scale, M, W, ldw, w_scale, N, K, bias, bias_dtype, Y, ldy, y_dtype, workspace, head,
-                      stream);
+  return q4_int8_gemm(codes, ldc, scale, M, W, ldw, w_scale, N, K, bias, bias_dtype, Y, ldy, y_dtype, workspace,
+                      workspace_bytes, stream);
 }
 
 int q4_kv_append(const q4_kv_cache *cache, const void *K, const void *V, int32_t dtype, int64_t tokens,

@@ -90,8 +90,8 @@ def library():
             "q4_int8_quantize_rows": ([P, i32, i64, i64, i64, P, i64, P, P], i32),
             "q4_int8_gemm_workspace_size": ([i64, i64, i64, ctypes.POINTER(sz)], i32),
             "q4_int8_gemm": ([P, i64, P, i64, P, i64, P, i64, i64, P, i32, P, i64, i32, P, sz, P], i32),
-            "q4_int8_linear_workspace_size": ([i64, i64, i64, ctypes.POINTER(sz)], i32),
-            "q4_int8_linear": ([P, i32, i64, i64, P, i64, P, i64, i64, P, i32, P, i64, i32, P, sz, P], i32),
+            "q4_int8_linear_scratch_size": ([i64, i64, ctypes.POINTER(sz)], i32),
+            "q4_int8_linear": ([P, i32, i64, i64, P, i64, P, i64, i64, P, i32, P, i64, i32, P, sz, P, sz, P], i32),
             "q4_kv_append": ([ctypes.POINTER(_CKVCache), P, P, i32, i64, i64, i64, i64, i64, P, P], i32),
             "q4_kv_dequantize": ([ctypes.POINTER(_CKVCache), P, i64, P, P, i32, P], i32),
             "q4_kv_attention_workspace_size": ([ctypes.POINTER(_CKVCache), i64, i64, i32, ctypes.POINTER(sz)], i32),
@@ -600,16 +600,16 @@ def _check_bias_out(bias, out, M, N, out_dtype, dev):
     return out
 
 
-_int8_ws_need = {}  # (M, N, K) -> workspace bytes of the product and of the linear layer
+_int8_ws_need = {}  # (M, N, K, device) -> workspace bytes of the product, scratch bytes of the linear layer
 
 
-def _int8_ws_sizes(M, N, K):
-    key = (M, N, K)
+def _int8_ws_sizes(M, N, K, device):
+    key = (M, N, K, device.index)
     need = _int8_ws_need.get(key)
     if need is None:
         a, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
         _check(library().q4_int8_gemm_workspace_size(M, N, K, ctypes.byref(a)), "q4_int8_gemm_workspace_size")
-        _check(library().q4_int8_linear_workspace_size(M, N, K, ctypes.byref(b)), "q4_int8_linear_workspace_size")
+        _check(library().q4_int8_linear_scratch_size(M, K, ctypes.byref(b)), "q4_int8_linear_scratch_size")
         if len(_int8_ws_need) >= 4096:
             _int8_ws_need.clear()
         need = _int8_ws_need[key] = (a.value, b.value)
@@ -633,7 +633,7 @@ def int8_gemm(A: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor, w_scale: 
     with _On(A, stream) as s:
         y = _check_bias_out(bias, out, M, N, out_dtype, A.device)
         if M and N:
-            ws = _stream_workspace(A.device, "int8", s, _int8_ws_sizes(M, N, K)[0])
+            ws = _stream_workspace(A.device, "int8", s, _int8_ws_sizes(M, N, K, A.device)[0])
             _check(library().q4_int8_gemm(
                 A.data_ptr(), A.stride(0), a_scale.data_ptr(), M, W.data_ptr(), W.stride(0), w_scale.data_ptr(), N, K,
                 None if bias is None else bias.data_ptr(), 0 if bias is None else _DT[bias.dtype], y.data_ptr(),
@@ -661,11 +661,14 @@ def int8_linear(X: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, bias: t
     with _On(X, stream) as s:
         y = _check_bias_out(bias, out, M, N, out_dtype, X.device)
         if M and N:
-            ws = _stream_workspace(X.device, "int8", s, _int8_ws_sizes(M, N, K)[1])
+            need, scratch_need = _int8_ws_sizes(M, N, K, X.device)
+            ws = _stream_workspace(X.device, "int8", s, need)
+            scratch = torch.empty(scratch_need, dtype=torch.uint8, device=X.device)
             _check(library().q4_int8_linear(
                 X.data_ptr(), _DT[X.dtype], max(X.stride(0), K), M, W.data_ptr(), W.stride(0), w_scale.data_ptr(), N,
                 K, None if bias is None else bias.data_ptr(), 0 if bias is None else _DT[bias.dtype], y.data_ptr(),
-                max(y.stride(0), N), _DT[out_dtype], ws.data_ptr(), ws.numel(), s), "q4_int8_linear")
+                max(y.stride(0), N), _DT[out_dtype], scratch.data_ptr(), scratch_need,
+                None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s), "q4_int8_linear")
     return y
 
 

@@ -363,9 +363,11 @@ Q4_API int q4_int8_quantize_rows(const void *X, int32_t x_dtype, int64_t rows, i
  *   bias   device, [N] of bias_dtype (Q4_F16 / Q4_BF16 / Q4_F32), or NULL.
  *   Y      device, y_dtype (Q4_F16 / Q4_BF16 / Q4_F32), rows ldy elements apart
  *          (>= N); what lies past N is left as it was.
- *   workspace  device, 16-byte aligned, q4_int8_gemm_workspace_size() bytes,
- *          zero-filled before its first use; every call leaves it zero-filled.
- *          Calls that run at once need workspaces of their own.
+ *   workspace  device, 16-byte aligned, q4_int8_gemm_workspace_size() bytes
+ *          (0 for some shapes; the size depends on the device's SM count),
+ *          zero-filled before its first use; every call leaves it zero-filled
+ *          (after a Q4_STATUS_TIMEOUT it must be zero-filled again).  Calls
+ *          that run at once need workspaces of their own.
  */
 Q4_API int q4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes);
 Q4_API int q4_int8_gemm(const int8_t *A, int64_t lda, const float *a_scale, int64_t M, const int8_t *W, int64_t ldw,
@@ -373,14 +375,14 @@ Q4_API int q4_int8_gemm(const int8_t *A, int64_t lda, const float *a_scale, int6
                         int64_t ldy, int32_t y_dtype, void *workspace, size_t workspace_bytes, void *stream);
 
 /* The linear layer on 16-bit activations X [M, K] (rows ldx elements apart):
- * q4_int8_quantize_rows into the workspace, then q4_int8_gemm; bit for bit
- * their results.  workspace: q4_int8_linear_workspace_size() bytes, with the
- * rules of q4_int8_gemm (its head is the GEMM's workspace, the codes and
- * scales of X follow and need no zero-fill). */
-Q4_API int q4_int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes);
+ * q4_int8_quantize_rows into `scratch`, then q4_int8_gemm; bit for bit their
+ * results.  scratch: device, 16-byte aligned, q4_int8_linear_scratch_size()
+ * bytes of any contents, used by this call only; workspace: as q4_int8_gemm's. */
+Q4_API int q4_int8_linear_scratch_size(int64_t M, int64_t K, size_t *bytes);
 Q4_API int q4_int8_linear(const void *X, int32_t x_dtype, int64_t ldx, int64_t M, const int8_t *W, int64_t ldw,
                           const float *w_scale, int64_t N, int64_t K, const void *bias, int32_t bias_dtype, void *Y,
-                          int64_t ldy, int32_t y_dtype, void *workspace, size_t workspace_bytes, void *stream);
+                          int64_t ldy, int32_t y_dtype, void *scratch, size_t scratch_bytes, void *workspace,
+                          size_t workspace_bytes, void *stream);
 
 /* ---- key/value cache in 4 bits, and attention over it ------------------- */
 

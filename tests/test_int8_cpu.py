@@ -27,9 +27,9 @@ def gemm(lib, Ap=A, lda=64, sa=A, M=4, W=A, ldw=64, sw=A, N=8, K=64, bias=None, 
     return lib.q4_int8_gemm(Ap, lda, sa, M, W, ldw, sw, N, K, bias, bdt, Y, ldy, ydt, ws, wsb, None)
 
 
-def linear(lib, X=A, dt=0, ldx=64, M=4, W=A, ldw=64, sw=A, N=8, K=64, bias=None, bdt=0, Y=A, ldy=8, ydt=0, ws=A,
-           wsb=1 << 40):
-    return lib.q4_int8_linear(X, dt, ldx, M, W, ldw, sw, N, K, bias, bdt, Y, ldy, ydt, ws, wsb, None)
+def linear(lib, X=A, dt=0, ldx=64, M=4, W=A, ldw=64, sw=A, N=8, K=64, bias=None, bdt=0, Y=A, ldy=8, ydt=0, scr=A,
+           scb=1 << 40, ws=A, wsb=1 << 40):
+    return lib.q4_int8_linear(X, dt, ldx, M, W, ldw, sw, N, K, bias, bdt, Y, ldy, ydt, scr, scb, ws, wsb, None)
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="made-up pointers: only where nothing can be launched")
@@ -47,20 +47,21 @@ def test_refusals(lib):
                    (dict(Ap=A + 8), ALIGN), (dict(W=A + 8), ALIGN)]:
         assert gemm(lib, **kw) == rc, kw
     for kw, rc in [(dict(X=None), ARG), (dict(dt=2), ARG), (dict(ldx=63), SHAPE), (dict(ldw=72), SHAPE),
-                   (dict(ldy=7), SHAPE), (dict(W=A + 8), ALIGN), (dict(ws=None), WORKSPACE), (dict(wsb=16), WORKSPACE),
-                   (dict(ws=A + 8), ALIGN)]:
+                   (dict(ldy=7), SHAPE), (dict(W=A + 8), ALIGN), (dict(scr=None), WORKSPACE), (dict(scb=16), WORKSPACE),
+                   (dict(ws=A + 8), ALIGN), (dict(scr=A + 8), ALIGN), (dict(K=4096, ldx=4096, ldw=4096, ws=None), WORKSPACE),
+                   (dict(K=4096, ldx=4096, ldw=4096, wsb=16), WORKSPACE)]:
         assert linear(lib, **kw) == rc, kw
 
 
 def test_workspace_sizes(lib):
     n = ctypes.c_size_t(0)
-    for M, N, K in [(1, 1, 1), (33, 4096, 4095), (4096, 28672, 8192)]:
+    for M, N, K in [(1, 1, 1), (1, 4096, 4096), (33, 4096, 4095), (300, 300, 300), (4096, 28672, 8192)]:
         assert lib.q4_int8_gemm_workspace_size(M, N, K, ctypes.byref(n)) == 0
-        head = n.value
-        assert lib.q4_int8_linear_workspace_size(M, N, K, ctypes.byref(n)) == 0
-        assert n.value >= head + 4 * M + M * ((K + 15) // 16 * 16)
+        assert n.value < 20 << 20  # less than one wave of tiles is cut
+        assert lib.q4_int8_linear_scratch_size(M, K, ctypes.byref(n)) == 0
+        assert n.value >= 4 * M + M * ((K + 15) // 16 * 16)
     assert lib.q4_int8_gemm_workspace_size(0, 1, 1, ctypes.byref(n)) == SHAPE
-    assert lib.q4_int8_linear_workspace_size(1, 1, 131072, ctypes.byref(n)) == SHAPE
+    assert lib.q4_int8_linear_scratch_size(1, 131072, ctypes.byref(n)) == SHAPE
     assert lib.q4_int8_gemm_workspace_size(1, 1, 1, None) == ARG
 
 
