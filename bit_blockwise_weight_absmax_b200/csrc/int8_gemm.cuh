@@ -20,9 +20,12 @@
 //
 // Work: tiles are dealt round robin in whole waves; what is left over (all of
 // them, for small products) is cut in k into equal runs of k-blocks, one per
-// CTA.  A cut tile's sums are added into the zeroed workspace (integers: any
-// order gives the same bits) and counted per epilogue warp in k-blocks; the
-// warp that completes a count writes Y and leaves its part zeroed again.
+// CTA.  The sums of an unfinished tile go to the workspace (a CTA has two at
+// most, at the ends of its run) and are counted per epilogue warp in
+// k-blocks; the warp that completes a count adds the others' to its own
+// (integers: any order gives the same bits), writes Y and zeroes the count.
+// (Adding them with atomics instead took 34 us for 128 x 256 tiles: 32-bit
+// atomics go at about one element per L2 slice and cycle.)
 //
 // The weights' first k-blocks are prefetched into L2 before the wait for the
 // previous kernel, so they travel while that kernel (the quantization of the
@@ -44,6 +47,7 @@ constexpr int kI8Rows = 128;                 // weight rows per CTA
 constexpr int kI8EpiWarps = 8;
 constexpr int kI8Threads = (2 + kI8EpiWarps) * 32;
 constexpr int kI8GroupT = 8;                 // token tiles that go together through the weight tiles
+constexpr size_t kI8CountBytes = Q4_WORKSPACE_HEAD;  // the counts' part of the workspace, at its start
 constexpr int kI8WTile = kI8Rows * kI8Bk;    // 16 KB
 
 template <int NT, bool PAIR> struct I8Shape {
@@ -71,8 +75,8 @@ struct alignas(64) I8GemmParams {
   int32_t cut_ctas;        // CTAs (pairs) that share the cut tiles
   int32_t stall_copies;    // test hook: the producer issues no copies
   int32_t prefetch;        // weight boxes prefetched into L2 before the wait
-  int32_t *sums;           // cut tiles' sums [slot][CTA of the pair][NT][128], zero between calls
-  unsigned *counts;        // [slot][CTA of the pair][epilogue warp] k-blocks, zero between calls
+  unsigned *counts;        // cut tiles: [slot][CTA of the pair][epilogue warp] k-blocks done, zero between calls
+  int32_t *parts;          // [CTA][first or last run][NT / 16][128 rows][16 tokens] sums of unfinished tiles
   uint64_t wait_ns;
   int *status;
 };
@@ -85,6 +89,8 @@ struct I8Item {
 struct I8Walk {
   int64_t u, u1;
   int tile;
+  int64_t first;  // the run's first unit
+  bool started;   // the current item is not the run's first
 };
 __device__ __forceinline__ I8Walk i8_walk(const I8GemmParams &p, int c) {
   I8Walk w;
@@ -92,7 +98,13 @@ __device__ __forceinline__ I8Walk i8_walk(const I8GemmParams &p, int c) {
   w.u = c < p.cut_ctas ? units * c / p.cut_ctas : 0;
   w.u1 = c < p.cut_ctas ? units * (c + 1) / p.cut_ctas : 0;
   w.tile = c;
+  w.started = false;
+  w.first = w.u;
   return w;
+}
+// CTA (pair) of the cut tiles' unit u.
+__device__ __forceinline__ int i8_owner(const I8GemmParams &p, int64_t units, int64_t u) {
+  return (int)(((u + 1) * p.cut_ctas - 1) / units);
 }
 __device__ __forceinline__ bool i8_next(const I8GemmParams &p, I8Walk &w, int g, I8Item &it) {
   if (w.u < w.u1) {
@@ -101,6 +113,7 @@ __device__ __forceinline__ bool i8_next(const I8GemmParams &p, I8Walk &w, int g,
     it.tile = p.whole + s;
     it.kb0 = (int)(w.u - (int64_t)s * p.nk);
     it.kb1 = (int)min((int64_t)p.nk, it.kb0 + (w.u1 - w.u));
+    w.started = w.u > w.first;
     w.u += it.kb1 - it.kb0;
     return true;
   }
@@ -375,47 +388,73 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
       tc_fence_after();
       const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * Sh::kCols);
       const bool cut = it.slot >= 0 && it.kb1 - it.kb0 < p.nk;
-      int32_t *sums = p.sums + ((int64_t)(it.slot * (PAIR ? 2 : 1) + rank) * NT) * kI8Rows + nl;
-#pragma unroll 1
-      for (int ch = ch0; ch < ch1 && 16 * ch < nt; ++ch) {
-        uint32_t r[16];
-        tmem_ld16(ta + 16 * ch, r);
-        if (!cut) {
-          i8_store16(p, n, tt * NT + 16 * ch, sw, bias, r);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (16 * ch + j < nt) atomicAdd(sums + (16 * ch + j) * kI8Rows, (int32_t)r[j]);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR) mbar_arrive_cluster(map_rank(accempty_bar(b), 0));
-        else mbar_arrive(accempty_bar(b));
-      }
-      if (cut && ch0 < ch1 && 16 * ch0 < nt) {
-        __threadfence();  // this lane's additions are visible before its warp's count
+      const bool mine = ch0 < ch1 && 16 * ch0 < nt;  // this warp has columns of the tile
+      auto release = [&] {
+        tc_fence_before();
         __syncwarp();
-        unsigned *cnt = p.counts + (it.slot * (PAIR ? 2 : 1) + rank) * kI8EpiWarps + (warp - 2);
+        if (lane == 0) {
+          if constexpr (PAIR) mbar_arrive_cluster(map_rank(accempty_bar(b), 0));
+          else mbar_arrive(accempty_bar(b));
+        }
+      };
+      if (!cut) {
+#pragma unroll 1
+        for (int ch = ch0; ch < ch1 && 16 * ch < nt; ++ch) {
+          uint32_t r[16];
+          tmem_ld16(ta + 16 * ch, r);
+          i8_store16(p, n, tt * NT + 16 * ch, sw, bias, r);
+        }
+        release();
+        continue;
+      }
+      // [CTA][run][chunk][row][16]: 64 bytes a lane and chunk
+      constexpr int kPer = PAIR ? 2 : 1;
+      auto part = [&](int cta, int run, int ch) {
+        return reinterpret_cast<int4 *>(p.parts + ((((int64_t)cta * kPer + rank) * 2 + run) * kChunks + ch) * kI8Rows * 16) + nl * 4;
+      };
+      bool last = false;
+      if (mine) {
+        const int run = it.kb0 == 0 && w.started ? 1 : 0;  // the run's second end, or its first
+#pragma unroll 1
+        for (int ch = ch0; ch < ch1 && 16 * ch < nt; ++ch) {
+          uint32_t r[16];
+          tmem_ld16(ta + 16 * ch, r);
+          int4 *dst = part(c, run, ch);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) __stcg(dst + v, make_int4((int)r[4 * v], (int)r[4 * v + 1], (int)r[4 * v + 2], (int)r[4 * v + 3]));
+        }
+        __threadfence();  // this lane's sums are visible before its warp's count
+        __syncwarp();
+        unsigned *cnt = p.counts + (it.slot * kPer + rank) * kI8EpiWarps + (warp - 2);
         unsigned old = 0;
         if (lane == 0) old = atomicAdd(cnt, (unsigned)(it.kb1 - it.kb0));
         old = __shfl_sync(0xffffffffu, old, 0);
-        if (old + (it.kb1 - it.kb0) == (unsigned)p.nk) {
-          __threadfence();
+        last = old + (it.kb1 - it.kb0) == (unsigned)p.nk;
+        if (last && lane == 0) *cnt = 0u;
+      }
+      if (last) {
+        __threadfence();
+        const int64_t units = (int64_t)(p.tiles_t * p.tiles_n - p.whole) * p.nk, u0 = (int64_t)it.slot * p.nk;
+        const int c0 = i8_owner(p, units, u0), c1 = i8_owner(p, units, u0 + p.nk - 1);
 #pragma unroll 1
-          for (int ch = ch0; ch < ch1 && 16 * ch < nt; ++ch) {
-            uint32_t r[16];
+        for (int ch = ch0; ch < ch1 && 16 * ch < nt; ++ch) {
+          uint32_t r[16];
+          tmem_ld16(ta + 16 * ch, r);
+#pragma unroll 1
+          for (int o = c0; o <= c1; ++o) {
+            if (o == c) continue;
+            // the tile is the end of a run that began before it, else the run's begin
+            const int4 *src = part(o, units * o / p.cut_ctas < u0 ? 1 : 0, ch);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) r[j] = 16 * ch + j < nt ? (uint32_t)__ldcg(sums + (16 * ch + j) * kI8Rows) : 0u;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (16 * ch + j < nt) __stcg(sums + (16 * ch + j) * kI8Rows, 0);
-            i8_store16(p, n, tt * NT + 16 * ch, sw, bias, r);
+            for (int v = 0; v < 4; ++v) {
+              const int4 t = __ldcg(src + v);
+              r[4 * v] += (uint32_t)t.x, r[4 * v + 1] += (uint32_t)t.y, r[4 * v + 2] += (uint32_t)t.z, r[4 * v + 3] += (uint32_t)t.w;
+            }
           }
-          if (lane == 0) *cnt = 0u;
+          i8_store16(p, n, tt * NT + 16 * ch, sw, bias, r);
         }
       }
+      release();
     }
   }
 

@@ -82,8 +82,11 @@ I8Plan int8_plan(int64_t M, int64_t N, int64_t K, int sms) {
   const int per = pl.pair ? 2 : 1;
   pl.grid = (int)(whole ? std::min<int64_t>(g, std::max<int64_t>(whole, cut)) : cut) * per;
   pl.slots = cut > rest ? (int)rest : 0;  // cut == rest: one whole tile each
-  pl.count_bytes = ((size_t)pl.slots * per * kI8EpiWarps * 4 + 255) & ~(size_t)255;
-  pl.ws_bytes = pl.slots ? pl.count_bytes + (size_t)pl.slots * per * pl.nt * kI8Rows * 4 : 0;
+  if (pl.slots * per * kI8EpiWarps * sizeof(unsigned) > kI8CountBytes) {  // more SMs than the counts have room for
+    pl.whole = (int)tiles, pl.cut_ctas = 0, pl.slots = 0;
+    pl.grid = (int)std::min<int64_t>(g, tiles) * per;
+  }
+  pl.ws_bytes = pl.slots ? kI8CountBytes + (size_t)pl.cut_ctas * per * 2 * pl.nt * kI8Rows * 4 : 0;
   return pl;
 }
 

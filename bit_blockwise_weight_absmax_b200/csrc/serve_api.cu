@@ -98,7 +98,7 @@ int q4_int8_gemm(const int8_t *A, int64_t lda, const float *a_scale, int64_t M, 
   p.whole = pl.whole, p.cut_ctas = pl.cut_ctas;
   p.prefetch = M <= 64 ? 16 : 4;
   p.counts = (unsigned *)workspace;
-  p.sums = (int32_t *)((char *)workspace + pl.count_bytes);
+  p.parts = (int32_t *)((char *)workspace + kI8CountBytes);
   p.stall_copies = g_copy_stall.load(std::memory_order_relaxed);
   p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   p.status = di.status;

@@ -17,7 +17,7 @@ struct I8Plan {
   bool pair = false; // 256-row tiles shared by two CTAs
   int tiles_t = 0, tiles_n = 0, whole = 0, cut_ctas = 0, grid = 0;
   int slots = 0;     // cut tiles
-  size_t count_bytes = 0, ws_bytes = 0;
+  size_t ws_bytes = 0;
 };
 I8Plan int8_plan(int64_t M, int64_t N, int64_t K, int sms);
 int run_int8_quantize(int dt, const I8QuantParams &p, cudaStream_t st);

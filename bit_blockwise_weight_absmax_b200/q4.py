@@ -504,43 +504,43 @@ def gemm(A: torch.Tensor, st: Q4State, out_dtype: torch.dtype | None = None, out
 # workspaces are one per device, kind and stream; a call that is captured into
 # a CUDA graph takes a workspace of its own, so graphs share none.
 
-class _On:
-    """Makes a tensor's device current, and `stream` when given, for a call."""
-    __slots__ = ("dev", "ctx")
-
-    def __init__(self, t: torch.Tensor, stream):
-        if not t.is_cuda:
-            raise Q4Error("no CUDA device: libq4 has no CPU fallback" if not torch.cuda.is_available()
-                          else "tensor must be on a CUDA device")
-        self.ctx = None
-        if stream is not None:
-            if stream.device != t.device:
-                raise Q4Error(f"stream is on {stream.device}, the tensors on {t.device}")
-            self.ctx = torch.cuda.stream(stream)
-        elif t.device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(t.device)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
-
-
-def _stream_workspace(device, kind: str, stream: int, nbytes: int) -> torch.Tensor | None:
-    """A zero-filled workspace for the current stream."""
-    if nbytes == 0:
+def _elsewhere(t: torch.Tensor, stream):
+    """None when t's device is current and no stream is given; otherwise the
+    context that makes them current, under which the caller calls itself."""
+    if stream is None and t.is_cuda and t.device.index == torch.cuda.current_device():
         return None
+    if not t.is_cuda:
+        raise Q4Error("no CUDA device: libq4 has no CPU fallback" if not torch.cuda.is_available()
+                      else "tensor must be on a CUDA device")
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise Q4Error(f"stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _current_stream(t: torch.Tensor) -> int:
+    """The handle of the current stream of t's device (torch.cuda.current_stream
+    builds an object for it, at 3 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+WORKSPACE_HEAD = 16384  # Q4_WORKSPACE_HEAD: the part of a workspace that starts zero-filled
+
+
+def _stream_workspace(device, stream: int, nbytes: int):
+    """(pointer, bytes, owner) of the current stream's workspace."""
+    if nbytes == 0:
+        return None, 0, None
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    key = (device.index, kind, stream)
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        t[:WORKSPACE_HEAD].zero_()
+        return t.data_ptr(), nbytes, t
+    key = (device.index, "stream", stream)
     t = _ws.get(key)
     if t is None or t.numel() < nbytes:
         t = _ws[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-    return t
+    return t.data_ptr(), t.numel(), t
 
 
 def _same_device(dev, **tensors):
@@ -567,16 +567,19 @@ def int8_quantize_rows(X: torch.Tensor, stream=None) -> tuple:
     rows, K = X.shape
     if K < 1:
         raise Q4Error("X has no columns")
+    ctx = _elsewhere(X, stream)
+    if ctx is not None:
+        with ctx:
+            return int8_quantize_rows(X)
     if X.stride(1) != 1 and K > 1 or rows > 1 and X.stride(0) < K:
         X = X.contiguous()
-    with _On(X, stream) as s:
-        ldc = (K + 15) // 16 * 16
-        codes = torch.empty(rows, ldc, dtype=torch.int8, device=X.device)[:, :K]
-        scale = torch.empty(rows, dtype=torch.float32, device=X.device)
-        if rows:
-            _check(library().q4_int8_quantize_rows(X.data_ptr(), _DT[X.dtype], rows, K, max(X.stride(0), K),
-                                                   codes.data_ptr(), ldc, scale.data_ptr(), s),
-                   "q4_int8_quantize_rows")
+    ldc = (K + 15) // 16 * 16
+    codes = torch.empty(rows, ldc, dtype=torch.int8, device=X.device)[:, :K]
+    scale = torch.empty(rows, dtype=torch.float32, device=X.device)
+    if rows:
+        _check(library().q4_int8_quantize_rows(X.data_ptr(), _DT[X.dtype], rows, K, max(X.stride(0), K),
+                                               codes.data_ptr(), ldc, scale.data_ptr(), _current_stream(X)),
+               "q4_int8_quantize_rows")
     return codes, scale
 
 
@@ -630,15 +633,18 @@ def int8_gemm(A: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor, w_scale: 
     if out_dtype not in _DT:
         raise Q4Error(f"out_dtype {out_dtype} is not float16, bfloat16 or float32")
     _same_device(A.device, a_scale=a_scale, W=W, w_scale=w_scale, bias=bias, out=out)
-    with _On(A, stream) as s:
-        y = _check_bias_out(bias, out, M, N, out_dtype, A.device)
-        if M and N:
-            ws = _stream_workspace(A.device, "int8", s, _int8_ws_sizes(M, N, K, A.device)[0])
-            _check(library().q4_int8_gemm(
-                A.data_ptr(), A.stride(0), a_scale.data_ptr(), M, W.data_ptr(), W.stride(0), w_scale.data_ptr(), N, K,
-                None if bias is None else bias.data_ptr(), 0 if bias is None else _DT[bias.dtype], y.data_ptr(),
-                max(y.stride(0), N), _DT[out_dtype], None if ws is None else ws.data_ptr(),
-                0 if ws is None else ws.numel(), s), "q4_int8_gemm")
+    ctx = _elsewhere(A, stream)
+    if ctx is not None:
+        with ctx:
+            return int8_gemm(A, a_scale, W, w_scale, bias, out_dtype, out)
+    y = _check_bias_out(bias, out, M, N, out_dtype, A.device)
+    if M and N:
+        s = _current_stream(A)
+        ws, ws_bytes, _ = _stream_workspace(A.device, s, _int8_ws_sizes(M, N, K, A.device)[0])
+        _check(library().q4_int8_gemm(
+            A.data_ptr(), A.stride(0), a_scale.data_ptr(), M, W.data_ptr(), W.stride(0), w_scale.data_ptr(), N, K,
+            None if bias is None else bias.data_ptr(), 0 if bias is None else _DT[bias.dtype], y.data_ptr(),
+            max(y.stride(0), N), _DT[out_dtype], ws, ws_bytes, s), "q4_int8_gemm")
     return y
 
 
@@ -656,19 +662,23 @@ def int8_linear(X: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor, bias: t
     if out_dtype not in _DT:
         raise Q4Error(f"out_dtype {out_dtype} is not float16, bfloat16 or float32")
     _same_device(X.device, W=W, w_scale=w_scale, bias=bias, out=out)
+    ctx = _elsewhere(X, stream)
+    if ctx is not None:
+        with ctx:
+            return int8_linear(X, W, w_scale, bias, out_dtype, out)
     if X.stride(1) != 1 and K > 1 or M > 1 and X.stride(0) < K:
         X = X.contiguous()
-    with _On(X, stream) as s:
-        y = _check_bias_out(bias, out, M, N, out_dtype, X.device)
-        if M and N:
-            need, scratch_need = _int8_ws_sizes(M, N, K, X.device)
-            ws = _stream_workspace(X.device, "int8", s, need)
-            scratch = torch.empty(scratch_need, dtype=torch.uint8, device=X.device)
-            _check(library().q4_int8_linear(
-                X.data_ptr(), _DT[X.dtype], max(X.stride(0), K), M, W.data_ptr(), W.stride(0), w_scale.data_ptr(), N,
-                K, None if bias is None else bias.data_ptr(), 0 if bias is None else _DT[bias.dtype], y.data_ptr(),
-                max(y.stride(0), N), _DT[out_dtype], scratch.data_ptr(), scratch_need,
-                None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s), "q4_int8_linear")
+    y = _check_bias_out(bias, out, M, N, out_dtype, X.device)
+    if M and N:
+        s = _current_stream(X)
+        need, scratch_need = _int8_ws_sizes(M, N, K, X.device)
+        ws, ws_bytes, _ = _stream_workspace(X.device, s, need)
+        scratch = torch.empty(scratch_need, dtype=torch.uint8, device=X.device) if scratch_need else None
+        _check(library().q4_int8_linear(
+            X.data_ptr(), _DT[X.dtype], max(X.stride(0), K), M, W.data_ptr(), W.stride(0), w_scale.data_ptr(), N, K,
+            None if bias is None else bias.data_ptr(), 0 if bias is None else _DT[bias.dtype], y.data_ptr(),
+            max(y.stride(0), N), _DT[out_dtype], None if scratch is None else scratch.data_ptr(), scratch_need, ws,
+            ws_bytes, s), "q4_int8_linear")
     return y
 
 
@@ -776,17 +786,21 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     """Quantize keys and values [tokens, kv_heads, head_dim] (fp16 or bf16) into
     the cache at slots (int64 [tokens], page * page_size + offset; a negative
     one passes its token over).  The slots of a call are distinct."""
-    with _On(k, stream) as s:
-        k = _head_rows(k, cache.kv_heads, cache.head_dim, "k")
-        v = _head_rows(v, cache.kv_heads, cache.head_dim, "v")
-        if k.shape != v.shape or k.dtype != v.dtype:
-            raise Q4Error("k and v must have one shape and dtype")
-        slots = _index(slots, torch.int64, (k.shape[0],), "slots")
-        _same_device(k.device, v=v, slots=slots, cache=cache)
-        if k.shape[0]:
-            _check(library().q4_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), _DT[k.dtype], k.shape[0],
-                                          k.stride(0), k.stride(1), v.stride(0), v.stride(1), slots.data_ptr(), s),
-                   "q4_kv_append")
+    ctx = _elsewhere(k, stream)
+    if ctx is not None:
+        with ctx:
+            return kv_append(cache, k, v, slots)
+    k = _head_rows(k, cache.kv_heads, cache.head_dim, "k")
+    v = _head_rows(v, cache.kv_heads, cache.head_dim, "v")
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise Q4Error("k and v must have one shape and dtype")
+    n = k.shape[0]
+    slots = _index(slots, torch.int64, (n,), "slots")
+    _same_device(k.device, v=v, slots=slots, cache=cache)
+    if n:
+        (kt, kh, _), (vt, vh, _) = k.stride(), v.stride()
+        _check(library().q4_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), _DT[k.dtype], n, kt, kh, vt, vh,
+                                      slots.data_ptr(), _current_stream(k)), "q4_kv_append")
 
 
 def kv_dequantize(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.float16, stream=None) -> tuple:
@@ -794,15 +808,18 @@ def kv_dequantize(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torc
     zeros for a negative slot."""
     if dtype not in (torch.float16, torch.bfloat16):
         raise Q4Error("dtype must be float16 or bfloat16")
-    with _On(slots, stream) as s:
-        slots = _index(slots, torch.int64, (None,), "slots")
-        _same_device(slots.device, cache=cache)
-        n = slots.shape[0]
-        k = torch.empty(n, cache.kv_heads, cache.head_dim, dtype=dtype, device=slots.device)
-        v = torch.empty_like(k)
-        if n:
-            _check(library().q4_kv_dequantize(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _DT[dtype],
-                                              s), "q4_kv_dequantize")
+    ctx = _elsewhere(slots, stream)
+    if ctx is not None:
+        with ctx:
+            return kv_dequantize(cache, slots, dtype)
+    slots = _index(slots, torch.int64, (None,), "slots")
+    _same_device(slots.device, cache=cache)
+    n = slots.shape[0]
+    k = torch.empty(n, cache.kv_heads, cache.head_dim, dtype=dtype, device=slots.device)
+    v = torch.empty_like(k)
+    if n:
+        _check(library().q4_kv_dequantize(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _DT[dtype],
+                                          _current_stream(slots)), "q4_kv_dequantize")
     return k, v
 
 
@@ -825,51 +842,54 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq
     cu_seqlens_q are left as they were (pass `out` to have them defined).
     Returns out [rows, q_heads, head_dim], with return_lse also float32 [rows,
     q_heads]."""
-    with _On(q, stream) as s:
-        dim = cache.head_dim
-        q = _head_rows(q, None, dim, "q")
-        rows, heads, _ = q.shape
-        if heads == 0 or heads % cache.kv_heads:
-            raise Q4Error(f"{heads} query heads are no multiple of {cache.kv_heads} key/value heads")
-        if window < 0:
-            raise Q4Error("window must be 0 (none) or positive")
-        seq_lens = _index(seq_lens, torch.int32, (None,), "seq_lens")
-        batch = seq_lens.shape[0]
-        if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch or \
-                block_table.shape[1] < 1:
-            raise Q4Error(f"block_table must be int32 [{batch}, pages], got {block_table.dtype} "
-                          f"{tuple(block_table.shape)}")
-        if block_table.stride(1) != 1 or block_table.stride(0) < block_table.shape[1]:
-            block_table = block_table.contiguous()
-        if cu_seqlens_q is not None:
-            cu_seqlens_q = _index(cu_seqlens_q, torch.int32, (batch + 1,), "cu_seqlens_q")
-        elif rows != batch:
-            raise Q4Error(f"{rows} query rows for {batch} sequences: pass cu_seqlens_q")
-        _same_device(q.device, cache=cache, block_table=block_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q,
-                     out=out)
-        if out is None:
-            out = torch.empty(rows, heads, dim, dtype=q.dtype, device=q.device)
-        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-            raise Q4Error("out must be a contiguous tensor of q's shape and dtype")
-        lse = torch.empty(rows, heads, dtype=torch.float32, device=q.device) if return_lse else None
-        if rows and batch:
-            key = (batch, rows, heads)
-            need = cache._ws_need.get(key)
-            if need is None:
-                n = ctypes.c_size_t(0)
-                _check(library().q4_kv_attention_workspace_size(cache._ref, batch, rows, heads, ctypes.byref(n)),
-                       "q4_kv_attention_workspace_size")
-                if len(cache._ws_need) >= 4096:
-                    cache._ws_need.clear()
-                need = cache._ws_need[key] = n.value
-            ws = _stream_workspace(q.device, "kv", s, need)
-            if max_q is None:
-                max_q = 1 if cu_seqlens_q is None else rows
-            _check(library().q4_kv_attention(
-                cache._ref, q.data_ptr(), _DT[q.dtype], rows, heads, q.stride(0), q.stride(1),
-                None if cu_seqlens_q is None else cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
-                block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]), block_table.shape[1], batch,
-                max(1, max_q), 1.0 / math.sqrt(dim) if scale is None else scale, int(causal), window, out.data_ptr(),
-                None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
-                0 if ws is None else ws.numel(), s), "q4_kv_attention")
+    ctx = _elsewhere(q, stream)
+    if ctx is not None:
+        with ctx:
+            return kv_attention(q, cache, block_table, seq_lens, cu_seqlens_q, max_q, scale, causal, window, out, return_lse)
+    dim = cache.head_dim
+    q = _head_rows(q, None, dim, "q")
+    rows, heads, _ = q.shape
+    if heads == 0 or heads % cache.kv_heads:
+        raise Q4Error(f"{heads} query heads are no multiple of {cache.kv_heads} key/value heads")
+    if window < 0:
+        raise Q4Error("window must be 0 (none) or positive")
+    seq_lens = _index(seq_lens, torch.int32, (None,), "seq_lens")
+    batch = seq_lens.shape[0]
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch or \
+            block_table.shape[1] < 1:
+        raise Q4Error(f"block_table must be int32 [{batch}, pages], got {block_table.dtype} "
+                      f"{tuple(block_table.shape)}")
+    if block_table.stride(1) != 1 or block_table.stride(0) < block_table.shape[1]:
+        block_table = block_table.contiguous()
+    if cu_seqlens_q is not None:
+        cu_seqlens_q = _index(cu_seqlens_q, torch.int32, (batch + 1,), "cu_seqlens_q")
+    elif rows != batch:
+        raise Q4Error(f"{rows} query rows for {batch} sequences: pass cu_seqlens_q")
+    _same_device(q.device, cache=cache, block_table=block_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q,
+                 out=out)
+    if out is None:
+        out = torch.empty(rows, heads, dim, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise Q4Error("out must be a contiguous tensor of q's shape and dtype")
+    lse = torch.empty(rows, heads, dtype=torch.float32, device=q.device) if return_lse else None
+    if rows and batch:
+        key = (batch, rows, heads)
+        need = cache._ws_need.get(key)
+        if need is None:
+            n = ctypes.c_size_t(0)
+            _check(library().q4_kv_attention_workspace_size(cache._ref, batch, rows, heads, ctypes.byref(n)),
+                   "q4_kv_attention_workspace_size")
+            if len(cache._ws_need) >= 4096:
+                cache._ws_need.clear()
+            need = cache._ws_need[key] = n.value
+        s = _current_stream(q)
+        ws, ws_bytes, _ = _stream_workspace(q.device, s, need)
+        if max_q is None:
+            max_q = 1 if cu_seqlens_q is None else rows
+        _check(library().q4_kv_attention(
+            cache._ref, q.data_ptr(), _DT[q.dtype], rows, heads, q.stride(0), q.stride(1),
+            None if cu_seqlens_q is None else cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
+            block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]), block_table.shape[1], batch,
+            max(1, max_q), 1.0 / math.sqrt(dim) if scale is None else scale, int(causal), window, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), ws, ws_bytes, s), "q4_kv_attention")
     return (out, lse) if return_lse else out

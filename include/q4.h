@@ -364,11 +364,14 @@ Q4_API int q4_int8_quantize_rows(const void *X, int32_t x_dtype, int64_t rows, i
  *   Y      device, y_dtype (Q4_F16 / Q4_BF16 / Q4_F32), rows ldy elements apart
  *          (>= N); what lies past N is left as it was.
  *   workspace  device, 16-byte aligned, q4_int8_gemm_workspace_size() bytes
- *          (0 for some shapes; the size depends on the device's SM count),
- *          zero-filled before its first use; every call leaves it zero-filled
- *          (after a Q4_STATUS_TIMEOUT it must be zero-filled again).  Calls
- *          that run at once need workspaces of their own.
+ *          (0 for some shapes; the size depends on the device's SM count).
+ *          Its first Q4_WORKSPACE_HEAD bytes are zero-filled before its first
+ *          use, and every call leaves them so (after a Q4_STATUS_TIMEOUT they
+ *          must be zero-filled again); the rest may hold anything.  One
+ *          workspace serves calls of all shapes in turn; calls that run at
+ *          once need their own.
  */
+#define Q4_WORKSPACE_HEAD 16384
 Q4_API int q4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes);
 Q4_API int q4_int8_gemm(const int8_t *A, int64_t lda, const float *a_scale, int64_t M, const int8_t *W, int64_t ldw,
                         const float *w_scale, int64_t N, int64_t K, const void *bias, int32_t bias_dtype, void *Y,
@@ -457,7 +460,8 @@ Q4_API int q4_kv_dequantize(const q4_kv_cache *cache, const int64_t *slots, int6
  *   lse    device, float [total_q][q_heads], log sum exp of the scaled
  *          scores, or NULL.
  *   max_q  the most rows of any sequence: it only helps to choose the kernel.
- *   workspace  as q4_int8_gemm's, q4_kv_attention_workspace_size() bytes.
+ *   workspace  as q4_int8_gemm's, q4_kv_attention_workspace_size() bytes (the
+ *          two may share one).
  * Entries outside the cache, lengths outside the table and row ranges outside
  * Q are cut off and set Q4_STATUS_INDEX.  The order of every sum is fixed by
  * the arguments and the device: identical calls give identical bits.
