@@ -76,7 +76,7 @@ struct alignas(64) I8GemmParams {
   int32_t stall_copies;    // test hook: the producer issues no copies
   int32_t prefetch;        // weight boxes prefetched into L2 before the wait
   unsigned *counts;        // cut tiles: [slot][CTA of the pair][epilogue warp] k-blocks done, zero between calls
-  int32_t *parts;          // [CTA][first or last run][NT / 16][128 rows][16 tokens] sums of unfinished tiles
+  int32_t *parts;          // sums of unfinished tiles: [CTA][first or last run][NT / 4][128 rows][4 tokens]
   uint64_t wait_ns;
   int *status;
 };
@@ -143,16 +143,23 @@ __device__ __forceinline__ float i8_bias(const void *bias, int dt, int64_t n) {
 
 // Outputs of weight row n for tokens t0 .. t0 + 15 from their integer sums:
 // sum to binary32, times the product of the scales, plus the bias, each
-// rounded once, then to y_dtype.  A warp's lanes are 32 adjacent n.
-__device__ __forceinline__ void i8_store16(const I8GemmParams &p, int n, int t0, float sw, float bias, const uint32_t (&r)[16]) {
+// rounded once, then to y_dtype.  sa: the tokens' scales, in shared memory.
+// A warp's lanes are 32 adjacent n.
+__device__ __forceinline__ void i8_store16(const I8GemmParams &p, int n, int t0, float sw, float bias, const float *sa,
+                                           const uint32_t (&r)[16]) {
   const int nt = min(16, p.M - t0);
   const int64_t at = (int64_t)t0 * p.ldy + n;
   float y[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float s = j < nt ? __ldcg(p.sa + t0 + j) : 0.0f;
-    y[j] = __fmul_rn((float)(int32_t)r[j], __fmul_rn(s, sw));
-    if (p.bias) y[j] = __fadd_rn(y[j], bias);
+  for (int v = 0; v < 4; ++v) {
+    const float4 s = reinterpret_cast<const float4 *>(sa)[v];
+    const float f[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = 4 * v + e;
+      y[j] = __fmul_rn((float)(int32_t)r[j], __fmul_rn(f[e], sw));
+      if (p.bias) y[j] = __fadd_rn(y[j], bias);
+    }
   }
   if (n >= p.N) return;
   if (p.y_dtype == Q4_F32) {
@@ -235,6 +242,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
   __shared__ uint64_t s_bar[2 * S + 4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ __align__(16) float s_sa[kI8EpiWarps][NT < 32 ? 16 : NT / 2];  // the token scales of each epilogue warp's columns
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = PAIR ? (int)(blockIdx.x & 1) : 0;
   const int c = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
@@ -384,6 +392,11 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
       const float sw = n < p.N ? __ldcg(p.sw + n) : 0.0f;
       const float bias = p.bias && n < p.N ? i8_bias(p.bias, p.bias_dtype, n) : 0.0f;
       const int nt = min(NT, p.M - tt * NT);  // tokens of the tile
+      float *sa = s_sa[warp - 2];  // of tokens tt * NT + 16 ch0 ..
+      __syncwarp();  // the previous tile's reads are done
+      for (int j = lane; j < 16 * (ch1 - ch0); j += 32)
+        sa[j] = 16 * ch0 + j < nt ? __ldcg(p.sa + tt * NT + 16 * ch0 + j) : 0.0f;
+      __syncwarp();
       if (!mbar_wait_warp(accfull_bar(b), (count >> 1) & 1, p.status, abort, p.wait_ns)) break;
       tc_fence_after();
       const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * Sh::kCols);
@@ -402,15 +415,15 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
         for (int ch = ch0; ch < ch1 && 16 * ch < nt; ++ch) {
           uint32_t r[16];
           tmem_ld16(ta + 16 * ch, r);
-          i8_store16(p, n, tt * NT + 16 * ch, sw, bias, r);
+          i8_store16(p, n, tt * NT + 16 * ch, sw, bias, sa + 16 * (ch - ch0), r);
         }
         release();
         continue;
       }
-      // [CTA][run][chunk][row][16]: 64 bytes a lane and chunk
+      // [CTA][run][chunk][4 tokens][row]: a warp's 16-byte accesses are adjacent
       constexpr int kPer = PAIR ? 2 : 1;
       auto part = [&](int cta, int run, int ch) {
-        return reinterpret_cast<int4 *>(p.parts + ((((int64_t)cta * kPer + rank) * 2 + run) * kChunks + ch) * kI8Rows * 16) + nl * 4;
+        return reinterpret_cast<int4 *>(p.parts + ((((int64_t)cta * kPer + rank) * 2 + run) * kChunks + ch) * kI8Rows * 16) + nl;
       };
       bool last = false;
       if (mine) {
@@ -421,7 +434,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
           tmem_ld16(ta + 16 * ch, r);
           int4 *dst = part(c, run, ch);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) __stcg(dst + v, make_int4((int)r[4 * v], (int)r[4 * v + 1], (int)r[4 * v + 2], (int)r[4 * v + 3]));
+          for (int v = 0; v < 4; ++v) __stcg(dst + v * kI8Rows, make_int4((int)r[4 * v], (int)r[4 * v + 1], (int)r[4 * v + 2], (int)r[4 * v + 3]));
         }
         __threadfence();  // this lane's sums are visible before its warp's count
         __syncwarp();
@@ -435,23 +448,46 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
       if (last) {
         __threadfence();
         const int64_t units = (int64_t)(p.tiles_t * p.tiles_n - p.whole) * p.nk, u0 = (int64_t)it.slot * p.nk;
-        const int c0 = i8_owner(p, units, u0), c1 = i8_owner(p, units, u0 + p.nk - 1);
+        const int c0 = i8_owner(p, units, u0), others = i8_owner(p, units, u0 + p.nk - 1) - c0;
+        // kOC of the others' sums of kCC chunks are on their way at once: one
+        // after the other their latencies were most of a small product's time
+        constexpr int kCC = kHalf >= 2 ? 2 : 1, kOC = kCC == 2 ? 2 : 4;
 #pragma unroll 1
-        for (int ch = ch0; ch < ch1 && 16 * ch < nt; ++ch) {
-          uint32_t r[16];
-          tmem_ld16(ta + 16 * ch, r);
-#pragma unroll 1
-          for (int o = c0; o <= c1; ++o) {
-            if (o == c) continue;
-            // the tile is the end of a run that began before it, else the run's begin
-            const int4 *src = part(o, units * o / p.cut_ctas < u0 ? 1 : 0, ch);
+        for (int ch = ch0; ch < ch1 && 16 * ch < nt; ch += kCC) {
+          uint32_t r[kCC][16];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const int4 t = __ldcg(src + v);
-              r[4 * v] += (uint32_t)t.x, r[4 * v + 1] += (uint32_t)t.y, r[4 * v + 2] += (uint32_t)t.z, r[4 * v + 3] += (uint32_t)t.w;
+          for (int e = 0; e < kCC; ++e)
+            if (ch + e < ch1) tmem_ld16(ta + 16 * (ch + e), r[e]);
+#pragma unroll 1
+          for (int o0 = 0; o0 < others; o0 += kOC) {
+            int4 t[kOC][kCC][4];
+#pragma unroll
+            for (int k = 0; k < kOC; ++k) {
+              const int o = c0 + o0 + k + (c0 + o0 + k >= c ? 1 : 0);  // the others, past this CTA
+              // the tile is the end of a run that began before it, else the run's begin
+              const int run = units * o / p.cut_ctas < u0 ? 1 : 0;
+#pragma unroll
+              for (int e = 0; e < kCC; ++e) {
+                const int4 *src = part(o, run, ch + e);
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                  t[k][e][v] = o0 + k < others && ch + e < ch1 ? __ldcg(src + v * kI8Rows) : make_int4(0, 0, 0, 0);
+              }
             }
+#pragma unroll
+            for (int k = 0; k < kOC; ++k)
+#pragma unroll
+              for (int e = 0; e < kCC; ++e)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                  r[e][4 * v] += (uint32_t)t[k][e][v].x, r[e][4 * v + 1] += (uint32_t)t[k][e][v].y;
+                  r[e][4 * v + 2] += (uint32_t)t[k][e][v].z, r[e][4 * v + 3] += (uint32_t)t[k][e][v].w;
+                }
           }
-          i8_store16(p, n, tt * NT + 16 * ch, sw, bias, r);
+#pragma unroll
+          for (int e = 0; e < kCC; ++e)
+            if (ch + e < ch1 && 16 * (ch + e) < nt)
+              i8_store16(p, n, tt * NT + 16 * (ch + e), sw, bias, sa + 16 * (ch + e - ch0), r[e]);
         }
       }
       release();

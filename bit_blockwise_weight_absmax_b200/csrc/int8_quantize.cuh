@@ -23,15 +23,53 @@ struct I8QuantParams {
 
 constexpr int kI8Keep = 4;
 
-// Four codes of four floats, low byte first.
-__device__ __forceinline__ uint32_t i8_codes4(const float *f, float s, float y, bool fast) {
-  uint32_t r = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float q = fast ? div_markstein(f[j], s, y) : __fdiv_rn(f[j], s);
-    r |= ((uint32_t)__float2int_rn(q) & 0xFFu) << (8 * j);
-  }
+// The scale of a row from its largest magnitude.
+struct I8Scale {
+  float s, y, stored;  // divisor, its reciprocal, the scale as stored (NaN for a bad row)
+  bool fast, zero, bad;
+};
+__device__ __forceinline__ I8Scale i8_scale(float top) {
+  I8Scale r;
+  r.bad = !(top <= 3.4028235e38f);
+  r.s = __fdiv_rn(top, 127.0f);
+  r.fast = markstein_ok(r.s);
+  r.y = r.fast ? __frcp_rn(r.s) : 0.0f;
+  r.zero = r.bad || r.s == 0.0f;
+  r.stored = r.bad ? __int_as_float(0x7FFFFFFF) : r.s;
   return r;
+}
+// max|x| of 8 elements as two bit patterns: both 16-bit formats order their
+// magnitudes as integers, infinities and NaNs last.
+__device__ __forceinline__ uint32_t i8_top8(uint4 v) {
+  const uint32_t a = __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), b = __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
+  return __vmaxu2(a, b);
+}
+// Codes of 8 elements.  |x / s| <= 127 (1 + 2^-23), so adding 1.5 * 2^23
+// rounds the quotient to the nearest integer, ties to even, and leaves its
+// 8-bit two's complement in the low byte.
+template <int DT> __device__ __forceinline__ uint2 i8_codes8(uint4 v, const I8Scale &c) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t b[8];
+  if (c.zero) return make_uint2(0, 0);
+  if (c.fast) {
+    const uint64_t yy = f2_pack(c.y, c.y), ns = f2_pack(-c.s, -c.s), kr = f2_pack(12582912.0f, 12582912.0f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float r0, r1;
+      f2_unpack(f2_add(div_markstein2(f2_pack(lo16<DT>(w[j]), hi16<DT>(w[j])), ns, yy), kr), r0, r1);
+      b[2 * j] = __float_as_uint(r0), b[2 * j + 1] = __float_as_uint(r1);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      b[2 * j] = (uint32_t)__float2int_rn(__fdiv_rn(lo16<DT>(w[j]), c.s));
+      b[2 * j + 1] = (uint32_t)__float2int_rn(__fdiv_rn(hi16<DT>(w[j]), c.s));
+    }
+  }
+  uint2 o;
+  o.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  o.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+  return o;
 }
 
 // VEC: rows start at 16-byte boundaries (8-element pieces are one load).
@@ -54,41 +92,25 @@ __global__ void __launch_bounds__(THREADS) int8_quantize_kernel(const __grid_con
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   };
-  // max|x| as a bit pattern: both 16-bit formats order their magnitudes as
-  // integers, infinities and NaNs last
-  auto top8 = [](uint4 v) -> uint32_t {
-    const uint32_t a = __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), b = __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
-    return __vmaxu2(a, b);
-  };
   uint4 keep[kI8Keep];
   uint32_t m2 = 0;
 #pragma unroll
   for (int k = 0; k < kI8Keep; ++k) {
     const int i = tid + k * THREADS;
     keep[k] = i < pieces ? load(i) : make_uint4(0, 0, 0, 0);
-    m2 = __vmaxu2(m2, top8(keep[k]));
+    m2 = __vmaxu2(m2, i8_top8(keep[k]));
   }
-  for (int i = tid + kI8Keep * THREADS; i < pieces; i += THREADS) m2 = __vmaxu2(m2, top8(load(i)));
+  for (int i = tid + kI8Keep * THREADS; i < pieces; i += THREADS) m2 = __vmaxu2(m2, i8_top8(load(i)));
   uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
   m = __reduce_max_sync(0xffffffffu, m);
   if ((tid & 31) == 0) s_max[tid >> 5] = m;
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < THREADS / 32; ++j) m = max(m, s_max[j]);
-  const float top = Dt<DT>::to_f((uint16_t)m);
-  const bool bad = !(top <= 3.4028235e38f);
-  const float s = __fdiv_rn(top, 127.0f);
-  const bool fast = markstein_ok(s);
-  const float y = fast ? __frcp_rn(s) : 0.0f;
-  const bool zero = bad || s == 0.0f;
+  const I8Scale sc = i8_scale(Dt<DT>::to_f((uint16_t)m));
   int8_t *c = p.codes + row * p.ldc;
   auto store = [&](int i, uint4 v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[2 * j] = lo16<DT>(w[j]), f[2 * j + 1] = hi16<DT>(w[j]);
-    uint2 o = make_uint2(0, 0);
-    if (!zero) o = make_uint2(i8_codes4(f, s, y, fast), i8_codes4(f + 4, s, y, fast));
+    const uint2 o = i8_codes8<DT>(v, sc);
     if (8 * i + 8 <= K) {
       reinterpret_cast<uint2 *>(c)[i] = o;
     } else {
@@ -102,8 +124,8 @@ __global__ void __launch_bounds__(THREADS) int8_quantize_kernel(const __grid_con
   }
   for (int i = tid + kI8Keep * THREADS; i < pieces; i += THREADS) store(i, load(i));
   if (tid == 0) {
-    p.scale[row] = bad ? __int_as_float(0x7FFFFFFF) : s;
-    if (bad) raise_status(p.status, Q4_STATUS_NONFINITE);
+    p.scale[row] = sc.stored;
+    if (sc.bad) raise_status(p.status, Q4_STATUS_NONFINITE);
   }
 }
 

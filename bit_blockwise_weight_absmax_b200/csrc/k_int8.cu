@@ -13,6 +13,8 @@ int go_quantize(const I8QuantParams &p, cudaStream_t st) {
   // a thread holds up to 32 elements: rows of up to 4096 take 128 threads
   if (p.cols <= 128 * 8 * kI8Keep) {
     launch_pdl(int8_quantize_kernel<DT, 128, VEC>, dim3((unsigned)p.rows), dim3(128), 0, st, p);
+  } else if (p.cols <= 256 * 8 * kI8Keep) {
+    launch_pdl(int8_quantize_kernel<DT, 256, VEC>, dim3((unsigned)p.rows), dim3(256), 0, st, p);
   } else {
     launch_pdl(int8_quantize_kernel<DT, 512, VEC>, dim3((unsigned)p.rows), dim3(512), 0, st, p);
   }
@@ -52,42 +54,87 @@ int run_int8_quantize(int dt, const I8QuantParams &p, cudaStream_t st) {
   return vec ? go_quantize<Q4_BF16, true>(p, st) : go_quantize<Q4_BF16, false>(p, st);
 }
 
-#ifndef I8_MIN_UNITS
-#define I8_MIN_UNITS 4
-#endif
+// The plan is the cheapest by this estimate (us, fitted to the measured
+// products of 64 .. 4096 tokens by 300 .. 28672 rows, which it meets within
+// about 15 %): a fixed part (set-up, first copies, last epilogue), the
+// k-blocks of the busiest CTA or the weights' way from memory, and the round
+// trip of sums where tiles are cut.
+struct I8Cost {
+  int nt;
+  float fixed, block, cut;
+};
+constexpr I8Cost kI8Costs[] = {
+    {16, 5.0f, 0.27f, 4.0f}, {32, 5.0f, 0.28f, 4.0f}, {64, 5.0f, 0.29f, 4.0f}, {128, 5.3f, 0.33f, 6.0f}, {256, 8.0f, 0.40f, 14.0f}};
+constexpr float kI8BytesPerUs = 6.4e6f;
+constexpr int kI8MinRun = 4;  // k-blocks a CTA takes of a cut tile, at least
+
 I8Plan int8_plan(int64_t M, int64_t N, int64_t K, int sms) {
-  I8Plan pl;
+  I8Plan best;
+  float best_us = 0.0f;
   const int nk = (int)((K + kI8Bk - 1) / kI8Bk);
-  pl.pair = M > 128;
-#ifdef I8_FORCE_NT
-  pl.pair = I8_FORCE_NT == 256;
-  pl.nt = I8_FORCE_NT;
-#else
-  pl.nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-#endif
-  const int rows = pl.pair ? 2 * kI8Rows : kI8Rows;
-  const int g = pl.pair ? sms / 2 : sms;
-  const int64_t tt = (M + pl.nt - 1) / pl.nt, tn = (N + rows - 1) / rows, tiles = tt * tn;
-  if (tiles > INT32_MAX / 2) {
-    pl.nt = 0;  // too many tiles for the kernel's indices
-    return pl;
+  for (const I8Cost &cost : kI8Costs) {
+    const bool pair = cost.nt == 256;
+    const int rows = pair ? 2 * kI8Rows : kI8Rows, g = pair ? sms / 2 : sms;
+    const int64_t tt = (M + cost.nt - 1) / cost.nt, tn = (N + rows - 1) / rows, tiles = tt * tn;
+    if (tiles > INT32_MAX / 2) continue;  // too many for the kernel's indices
+    const float bytes_us = (float)N * (float)K / kI8BytesPerUs;
+    for (int c = 0; c < 2; ++c) {
+      int64_t whole = tiles, cut = 0, rest = 0;
+      float blocks = (float)((tiles + g - 1) / g * nk);
+      if (c) {
+        whole = tiles / g * g;
+        rest = tiles - whole;
+        // an equal number of CTAs for each tile where that keeps most of them
+        // busy (then none has two unfinished tiles), else all CTAs
+        const int64_t most = nk / kI8MinRun, each = rest ? std::min<int64_t>(g / rest, most) : 0;
+        if (!rest || most < 2) continue;
+        cut = each >= 2 && (each == most || each * rest * 4 >= 3 * (int64_t)g) ? each * rest
+                                                                              : std::min<int64_t>(g, rest * most);
+        if (cut <= rest) continue;
+        blocks = (float)(whole / g * nk) + (float)(rest * nk) / (float)cut;
+      }
+      const float us = cost.fixed + std::max(blocks * cost.block, bytes_us) + (c ? cost.cut : 0.0f);
+      if (best.nt && us >= best_us) continue;
+      best_us = us;
+      best.nt = cost.nt;
+      best.pair = pair;
+      best.tiles_t = (int)tt, best.tiles_n = (int)tn;
+      best.whole = (int)whole, best.cut_ctas = (int)cut;
+      best.slots = (int)rest;
+      const int per = pair ? 2 : 1;
+      best.grid = (int)std::min<int64_t>(g, std::max(whole, cut)) * per;
+      best.ws_bytes = rest ? kI8CountBytes + (size_t)cut * per * 2 * cost.nt * kI8Rows * 4 : 0;
+      if ((size_t)rest * per * kI8EpiWarps * sizeof(unsigned) > kI8CountBytes) best.nt = 0;  // not on a B200's SMs
+    }
   }
-  pl.tiles_t = (int)tt, pl.tiles_n = (int)tn;
-  int64_t whole = tiles / g * g;
-  const int64_t rest = tiles - whole;
-  int64_t cut = rest == 0 ? 0 : std::min<int64_t>(g, std::max<int64_t>(rest, rest * nk / I8_MIN_UNITS));
-  if (rest * 8 >= (int64_t)g * 7) whole = tiles, cut = 0;  // the last wave is nearly full
-  pl.whole = (int)whole;
-  pl.cut_ctas = (int)cut;
-  const int per = pl.pair ? 2 : 1;
-  pl.grid = (int)(whole ? std::min<int64_t>(g, std::max<int64_t>(whole, cut)) : cut) * per;
-  pl.slots = cut > rest ? (int)rest : 0;  // cut == rest: one whole tile each
-  if (pl.slots * per * kI8EpiWarps * sizeof(unsigned) > kI8CountBytes) {  // more SMs than the counts have room for
-    pl.whole = (int)tiles, pl.cut_ctas = 0, pl.slots = 0;
-    pl.grid = (int)std::min<int64_t>(g, tiles) * per;
-  }
-  pl.ws_bytes = pl.slots ? kI8CountBytes + (size_t)pl.cut_ctas * per * 2 * pl.nt * kI8Rows * 4 : 0;
-  return pl;
+  return best;
+}
+
+namespace {
+template <int MT, int DT, bool VEC>
+int go_gemv(const I8GemvParams &p, int sms, cudaStream_t st) {
+  const int smem = MT * ((p.K + 15) / 16 * 16);
+  // as many CTAs of 8 warps as the SMs hold, a warp for each row where there are fewer
+  const int grid = (int)std::min<int64_t>((p.N + 7) / 8, (int64_t)i8v_ctas(MT) * sms);
+  launch_pdl(int8_gemv_kernel<MT, DT, VEC>, dim3((unsigned)grid), dim3(kI8vThreads), smem, st, p);
+  return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
+}
+template <int DT, bool VEC>
+int gemv_tokens(const I8GemvParams &p, int sms, cudaStream_t st) {
+  if (p.M == 1) return go_gemv<1, DT, VEC>(p, sms, st);
+  if (p.M == 2) return go_gemv<2, DT, VEC>(p, sms, st);
+  return go_gemv<4, DT, VEC>(p, sms, st);
+}
+}  // namespace
+
+bool int8_gemv_ok(int64_t M, int64_t K) {
+  return M <= kI8vMaxTokens && (M == 3 ? 4 : M) * ((K + 15) / 16 * 16) <= kI8vMaxBytes;
+}
+int run_int8_gemv(int x_dtype, const I8GemvParams &p, int sms, cudaStream_t st) {
+  if (!p.X) return gemv_tokens<-1, true>(p, sms, st);
+  const bool vec = ((uintptr_t)p.X & 15u) == 0 && p.ldx % 8 == 0;
+  if (x_dtype == Q4_F16) return vec ? gemv_tokens<Q4_F16, true>(p, sms, st) : gemv_tokens<Q4_F16, false>(p, sms, st);
+  return vec ? gemv_tokens<Q4_BF16, true>(p, sms, st) : gemv_tokens<Q4_BF16, false>(p, sms, st);
 }
 
 int run_int8_gemm(const I8Operands &o, const I8Plan &pl, I8GemmParams &p, cudaStream_t st) {

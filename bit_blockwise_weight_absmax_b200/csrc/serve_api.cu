@@ -27,6 +27,15 @@ int check_linear(int64_t M, int64_t N, int64_t K) {
   return Q4_OK;
 }
 
+void set_gemv(I8GemvParams &v, int64_t M, const int8_t *W, int64_t ldw, const float *w_scale, int64_t N, int64_t K,
+              const void *bias, int32_t bias_dtype, void *Y, int64_t ldy, int32_t y_dtype, int *status) {
+  v.W = W, v.ldw = ldw, v.sw = w_scale;
+  v.bias = bias, v.bias_dtype = bias_dtype;
+  v.Y = Y, v.ldy = ldy, v.y_dtype = y_dtype;
+  v.M = (int32_t)M, v.N = (int32_t)N, v.K = (int32_t)K;
+  v.status = status;
+}
+
 int check_cache(const q4_kv_cache *c, KvView *v) {
   if (!c || !c->k_codes || !c->k_state || !c->v_codes || !c->v_state) return Q4_ERR_ARG;
   if ((c->head_dim != 64 && c->head_dim != 128) || (c->blocksize != 64 && c->blocksize != 128) ||
@@ -68,6 +77,8 @@ int q4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes) 
   if (!bytes) return Q4_ERR_ARG;
   const int rc = check_linear(M, N, K);
   if (rc != Q4_OK) return rc;
+  *bytes = 0;
+  if (int8_gemv_ok(M, K)) return Q4_OK;
   const I8Plan pl = int8_plan(M, N, K, plan_sms());
   if (!pl.nt) return Q4_ERR_SHAPE;
   *bytes = pl.ws_bytes;
@@ -83,6 +94,13 @@ int q4_int8_gemm(const int8_t *A, int64_t lda, const float *a_scale, int64_t M, 
   if (lda < K || ldw < K || ldy < N || lda % 16 || ldw % 16) return Q4_ERR_SHAPE;
   if (!aligned16(A) || !aligned16(W) || !aligned16(workspace)) return Q4_ERR_ALIGN;
   const DeviceInfo di = device_info();
+  if (int8_gemv_ok(M, K)) {
+    if (di.ok != Q4_OK) return di.ok;
+    I8GemvParams v = {};
+    v.A = A, v.lda = lda, v.sa = a_scale;
+    set_gemv(v, M, W, ldw, w_scale, N, K, bias, bias_dtype, Y, ldy, y_dtype, di.status);
+    return run_int8_gemv(0, v, di.sms, (cudaStream_t)stream);
+  }
   const I8Plan pl = int8_plan(M, N, K, di.ok == Q4_OK ? di.sms : kDefaultSms);
   if (!pl.nt) return Q4_ERR_SHAPE;
   if (pl.ws_bytes && (!workspace || workspace_bytes < pl.ws_bytes)) return Q4_ERR_WORKSPACE;
@@ -110,7 +128,7 @@ int q4_int8_linear_scratch_size(int64_t M, int64_t K, size_t *bytes) {
   if (!bytes) return Q4_ERR_ARG;
   const int rc = check_linear(M, 1, K);
   if (rc != Q4_OK) return rc;
-  *bytes = up256((size_t)M * 4) + (size_t)M * ((size_t)(K + 15) / 16 * 16);
+  *bytes = int8_gemv_ok(M, K) ? 0 : up256((size_t)M * 4) + (size_t)M * ((size_t)(K + 15) / 16 * 16);
   return Q4_OK;
 }
 
@@ -126,7 +144,15 @@ int q4_int8_linear(const void *X, int32_t x_dtype, int64_t ldx, int64_t M, const
   if (rc != Q4_OK) return rc;
   if (ldx < K || ldw < K || ldw % 16 || ldy < N) return Q4_ERR_SHAPE;
   if (!aligned16(W) || !aligned16(workspace) || !aligned16(scratch)) return Q4_ERR_ALIGN;
-  if (!scratch || scratch_bytes < need || (head && (!workspace || workspace_bytes < head))) return Q4_ERR_WORKSPACE;
+  if ((need && (!scratch || scratch_bytes < need)) || (head && (!workspace || workspace_bytes < head))) return Q4_ERR_WORKSPACE;
+  if (int8_gemv_ok(M, K)) {
+    const DeviceInfo di = device_info();
+    if (di.ok != Q4_OK) return di.ok;
+    I8GemvParams v = {};
+    v.X = (const uint16_t *)X, v.ldx = ldx;
+    set_gemv(v, M, W, ldw, w_scale, N, K, bias, bias_dtype, Y, ldy, y_dtype, di.status);
+    return run_int8_gemv(x_dtype, v, di.sms, (cudaStream_t)stream);
+  }
   const int64_t ldc = (K + 15) / 16 * 16;
   float *scale = (float *)scratch;
   int8_t *codes = (int8_t *)scratch + up256((size_t)M * 4);

@@ -2,6 +2,7 @@
 // key/value-cache kernels (not part of the public C ABI).
 #pragma once
 #include "int8_gemm.cuh"
+#include "int8_gemv.cuh"
 #include "int8_quantize.cuh"
 #include "kv_attention.cuh"
 #include "kv_cache.cuh"
@@ -21,6 +22,9 @@ struct I8Plan {
 };
 I8Plan int8_plan(int64_t M, int64_t N, int64_t K, int sms);
 int run_int8_quantize(int dt, const I8QuantParams &p, cudaStream_t st);
+// Whether M tokens of K take the one-launch kernel of int8_gemv.cuh.
+bool int8_gemv_ok(int64_t M, int64_t K);
+int run_int8_gemv(int x_dtype, const I8GemvParams &p, int sms, cudaStream_t st);
 int run_int8_gemm(const I8Operands &o, const I8Plan &pl, I8GemmParams &p, cudaStream_t st);
 int run_kv_append(int dt, int D, int B, const KvAppendParams &p, cudaStream_t st);
 int run_kv_dequantize(int dt, int D, int B, const KvDequantParams &p, cudaStream_t st);

@@ -47,9 +47,10 @@ def test_refusals(lib):
                    (dict(Ap=A + 8), ALIGN), (dict(W=A + 8), ALIGN)]:
         assert gemm(lib, **kw) == rc, kw
     for kw, rc in [(dict(X=None), ARG), (dict(dt=2), ARG), (dict(ldx=63), SHAPE), (dict(ldw=72), SHAPE),
-                   (dict(ldy=7), SHAPE), (dict(W=A + 8), ALIGN), (dict(scr=None), WORKSPACE), (dict(scb=16), WORKSPACE),
-                   (dict(ws=A + 8), ALIGN), (dict(scr=A + 8), ALIGN), (dict(K=4096, ldx=4096, ldw=4096, ws=None), WORKSPACE),
-                   (dict(K=4096, ldx=4096, ldw=4096, wsb=16), WORKSPACE)]:
+                   (dict(ldy=7), SHAPE), (dict(W=A + 8), ALIGN), (dict(M=9, scr=None), WORKSPACE),
+                   (dict(M=9, scb=16), WORKSPACE), (dict(ws=A + 8), ALIGN), (dict(scr=A + 8), ALIGN),
+                   (dict(M=9, K=4096, ldx=4096, ldw=4096, ws=None), WORKSPACE),
+                   (dict(M=9, K=4096, ldx=4096, ldw=4096, wsb=16), WORKSPACE)]:
         assert linear(lib, **kw) == rc, kw
 
 
@@ -59,7 +60,7 @@ def test_workspace_sizes(lib):
         assert lib.q4_int8_gemm_workspace_size(M, N, K, ctypes.byref(n)) == 0
         assert n.value <= q4.WORKSPACE_HEAD + 148 * 2 * 256 * 128 * 4  # two unfinished tiles of 128 x 256 a CTA
         assert lib.q4_int8_linear_scratch_size(M, K, ctypes.byref(n)) == 0
-        assert n.value >= 4 * M + M * ((K + 15) // 16 * 16)
+        assert n.value >= 4 * M + M * ((K + 15) // 16 * 16) or (M <= 4 and n.value == 0)  # few tokens need none
     assert lib.q4_int8_gemm_workspace_size(0, 1, 1, ctypes.byref(n)) == SHAPE
     assert lib.q4_int8_linear_scratch_size(1, 131072, ctypes.byref(n)) == SHAPE
     assert lib.q4_int8_gemm_workspace_size(1, 1, 1, None) == ARG

@@ -97,7 +97,9 @@ def product_reference(A, sa, W, sw, bias):
 
 MNK = [(1, 1, 1), (1, 8, 16), (1, 128, 4096), (2, 129, 31), (3, 577, 1000), (16, 256, 129), (17, 100, 128), (31, 1536, 576),
        (33, 127, 127), (64, 640, 255), (65, 130, 2048), (127, 300, 64), (129, 257, 513), (256, 128, 1024), (257, 513, 385),
-       (512, 384, 4096), (700, 1111, 333), (2, 4096, 8192)]
+       (512, 384, 4096), (700, 1111, 333), (2, 4096, 8192),
+       (4, 50, 20000), (3, 2000, 12272), (5, 4096, 4096), (24, 11008, 1000), (513, 11008, 640), (1024, 2304, 4224),
+       (130, 20000, 2064)]
 
 
 @pytest.mark.parametrize("M,N,K", MNK)
@@ -173,6 +175,30 @@ def test_other_streams_and_graphs_that_run_at_once(q4):
                 graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("M,N,K", [(9, 600, 4096), (100, 4096, 4096), (1024, 1024, 8192)])
+def test_wait_limit_times_out_and_recovers(q4, M, N, K):
+    """With the copy-stall hook on no stage is ever filled: the waits run out, the call reports it, and after the
+    workspaces are zeroed again the next call is right (single CTAs, and CTA pairs for many tokens)."""
+    g = torch.Generator().manual_seed(8)
+    A, sa = random_codes(g, M, K)
+    W, sw = random_codes(g, N, K)
+    try:
+        q4.set_wait_limit_ns(200_000)
+        q4.set_copy_stall(True)
+        q4.int8_gemm(A, sa, W, sw, None, torch.float32)
+        torch.cuda.synchronize()
+        assert q4.last_device_status() & 2  # Q4_STATUS_TIMEOUT
+    finally:
+        q4.set_copy_stall(False)
+        q4.set_wait_limit_ns(0)
+        q4.reset_workspaces()
+        q4.clear_device_status()
+    y = q4.int8_gemm(A, sa, W, sw, None, torch.float32)
+    ref, err = product_reference(A, sa, W, sw, None)
+    assert ((y.double() - ref).abs() <= err).all()
+    assert q4.last_device_status() == 0
 
 
 def test_linear8bit_and_replace_linear(q4):
