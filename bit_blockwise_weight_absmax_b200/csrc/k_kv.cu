@@ -36,12 +36,23 @@ struct Dequant {
     return launched();
   }
 };
+// Rows that share a kv head: up to 8 take one column tile of the MMAs, more
+// take two at once (the cache is then read half as often).
+template <int DT, int D, int B, int NT>
+int go_attend(const KvAttnParams &p, int sms, cudaStream_t st) {
+  using Sh = KvShape<D, B, NT>;
+  constexpr auto kern = kv_attention_kernel<DT, D, B, NT>;
+  const int rc = set_smem_attr_once<kern>(Sh::kSmem, true);
+  if (rc != Q4_OK) return rc;
+  launch_pdl(kern, dim3((unsigned)(Sh::kCtas * sms)), dim3(kKvAttnThreads), Sh::kSmem, st, p);
+  return launched();
+}
 struct Attend {
   const KvAttnParams &p;
+  int rows, sms;
   cudaStream_t st;
   template <int DT, int D, int B> int operator()() const {
-    launch_pdl(kv_attention_kernel<DT, D, B>, dim3((unsigned)p.total_q, (unsigned)((p.q_heads + 3) / 4)), dim3(128), 0, st, p);
-    return launched();
+    return rows <= 8 ? go_attend<DT, D, B, 1>(p, sms, st) : go_attend<DT, D, B, 2>(p, sms, st);
   }
 };
 }  // namespace
@@ -50,5 +61,11 @@ int run_kv_append(int dt, int D, int B, const KvAppendParams &p, cudaStream_t st
 int run_kv_dequantize(int dt, int D, int B, const KvDequantParams &p, cudaStream_t st) {
   return by_format(dt, D, B, Dequant{p, st});
 }
-int run_kv_attention(int dt, int D, int B, const KvAttnParams &p, cudaStream_t st) { return by_format(dt, D, B, Attend{p, st}); }
+int run_kv_attention(int dt, int D, int B, const KvAttnParams &p, int64_t max_q, int sms, cudaStream_t st) {
+  const int64_t rows = max_q * (p.q_heads / p.c.heads);
+  return by_format(dt, D, B, Attend{p, rows <= 8 ? 8 : 16, sms, st});
+}
+size_t kv_attention_ws(int D, int sms) {
+  return kKvCountBytes + (size_t)2 * sms * 2 * 16 * (D + 2) * sizeof(float);
+}
 }  // namespace q4

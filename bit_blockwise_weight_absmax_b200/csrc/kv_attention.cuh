@@ -1,5 +1,31 @@
-// kv_attention.cuh -- softmax(scale Q K^T) V over the paged 4-bit cache (sm_100a).
+// kv_attention.cuh -- softmax(scale Q K^T) V over the paged 4-bit cache: the
+// kernel for single and few query rows (sm_100a).
+//
+// Bound by the cache's bytes (D + 8 D / B per key and head) and, close behind,
+// by issue: so the codes go into the tensor cores as they are.
+//  - A 4-bit code masked out of a packed word is a binary16 number already:
+//    w & 0x000f000f holds two codes as multiples of 2^-24 (binary16
+//    subnormals, which the MMAs take exactly), w & 0x00f000f0 two more times
+//    16.  Eight codes cost 5 integer instructions and no conversion.  The
+//    factors 2^24 and 16 go into the query and the output.
+//  - s (q - z) = s q - s z: per block, score = s_k (acc - z_k sum(Q)), and the
+//    values' scale goes into the weights: w = p s_v, O = sum w code - sum w z_v.
+//  - mma.sync m16n8k16, keys on the 16-row side, query rows (8 or 16 of the
+//    rows that share a kv head) on the 8-column side.  The contraction over d
+//    may run in any order, so a lane takes the words of a row as they lie.
+//  - Online softmax in base 2 with the running maximum of score +
+//    exponent(s_v): the weights w <= 2^9 then use binary16's range well
+//    whatever the values' sizes.  Query rows are scaled by a power of two into
+//    binary16 (exact for both 16-bit types down to 2^-38 of the row's largest).
+// Work: the (sequence, row tile, kv head) segments, each in units of 32 keys,
+// are one list that is cut into equal runs, one per CTA, whatever the lengths;
+// a CTA's 8 warps take its units in turn, each with its own ring of bulk
+// copies.  Warps join through shared memory; a segment's CTAs join through the
+// workspace, the last to arrive in the order of the keys.  (tcgen05 has no
+// tile below 128 rows on the key side that would pay for 8 query rows, and
+// needs dequantized operands in shared memory; here registers feed the MMAs.)
 #pragma once
+#include "gemm.cuh"  // PTX wrappers, bounded waits
 #include "kv_cache.cuh"
 
 namespace q4 {
@@ -16,6 +42,9 @@ struct KvAttnParams {
   int32_t causal, window;  // window 0: none
   uint16_t *out;
   float *lse;
+  unsigned *counts;  // [CTA] arrivals at the segment that the CTA is the first of, zero between calls
+  float *parts;      // [CTA][first or last segment][kPart] results of cut segments
+  uint64_t wait_ns;
   int *status;
 };
 
@@ -43,77 +72,586 @@ __device__ __forceinline__ int kv_page(const KvAttnParams &p, int b, int i, int6
   return -1;
 }
 
-// One warp for a (row, query head): lanes take keys in turn, each with its own
-// running maximum, sum and (in shared memory) none: the values are summed in a
-// second pass over the keys with the finished maximum.
-template <int DT, int D, int B>
-__global__ void __launch_bounds__(128) kv_attention_kernel(const __grid_constant__ KvAttnParams p) {
-  pdl_launch_then_wait();
-  constexpr int NB = D / B, W = D / 8;
-  __shared__ float sq[4][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y * 4 + warp;
-  const int row = blockIdx.x;
-  int b = 0;
-  KvSeq s = {0, 0, 0};
-  bool found = false;
-  for (b = 0; b < p.batch; ++b) {
-    s = kv_seq(p, b);
-    if (row >= s.q0 && row < s.q0 + s.n) {
-      found = true;
-      break;
-    }
+
+constexpr int kKvUnit = 32;    // keys per unit
+constexpr int kKvWarps = 8;
+constexpr int kKvMinUnits = 8; // units a CTA takes at least: one for each warp
+constexpr float kKvSlack = 8.0f;
+constexpr int kKvAttnThreads = kKvWarps * 32;
+constexpr size_t kKvCountBytes = Q4_WORKSPACE_HEAD;
+
+template <int D, int B, int NT> struct KvShape {
+  static constexpr int NB = D / B, R = 8 * NT;
+  static constexpr int kCodes = kKvUnit * D / 2, kState = kKvUnit * NB * 4;  // bytes of K or V in a unit
+  static constexpr int kStage = 2 * (kCodes + kState);
+  static constexpr int kCtas = NT == 1 ? 2 : 1;  // per SM: two column tiles need more than 128 registers
+  static constexpr int kStages = NT == 1 ? 2 : 4;
+  static constexpr int kQRow = D * 2 + 16;   // bytes of a query row in shared memory
+  static constexpr int kORow = D + 4;        // floats of an output row
+  static constexpr int kRing = kKvWarps * kStages * kStage;
+  static constexpr int kSmem = kRing + R * kQRow + 4 * R * kORow * 4 + 2 * kKvWarps * R * 4;
+  static constexpr int kPart = R * (D + 2);  // floats of a partial result: O, then M and l
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transposes an 8 x 8 matrix of 16-bit values held two to a lane.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float half_lo(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu))); }
+__device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w >> 16))); }
+__device__ __forceinline__ void kv_bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+      "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// The units of sequence b: u0 .. u0 + units - 1 (at least one where it has
+// rows, so that empty rows are written) for each of rt row tiles.
+struct KvSpan {
+  KvSeq s;
+  int u0, units, rt;
+};
+template <int R> __device__ __forceinline__ KvSpan kv_span(const KvAttnParams &p, int b, int group) {
+  KvSpan v;
+  v.s = kv_seq(p, b);
+  v.rt = (int)(((int64_t)v.s.n * group + R - 1) / R);
+  const int lo = p.window ? max(0, v.s.len - v.s.n - p.window + 1) : 0;
+  v.u0 = lo / kKvUnit;
+  v.units = v.s.n > 0 ? max(1, (v.s.len + kKvUnit - 1) / kKvUnit - v.u0) : 0;
+  return v;
+}
+
+template <int DT, int D, int B, int NT>
+__global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_attention_kernel(const __grid_constant__ KvAttnParams p) {
+  using Sh = KvShape<D, B, NT>;
+  constexpr int NB = Sh::NB, R = Sh::R, W4 = D / 32;  // W4: words of a key a lane takes
+  constexpr int MT = D / 16;                          // 16-row tiles of the output's d
+  pdl_launch_dependents();
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t *s_q = smem + Sh::kRing;
+  float *s_o = reinterpret_cast<float *>(s_q + R * Sh::kQRow);  // [4][R][kORow]
+  float *s_m = s_o + 4 * R * Sh::kORow, *s_l = s_m + kKvWarps * R;
+  __shared__ uint64_t s_bar[kKvWarps * Sh::kStages];
+  __shared__ float s_hf[R], s_qs[NB][R];
+  __shared__ int64_t s_scan[kKvWarps + 1], s_first[2];
+  __shared__ int s_abort;
+  __shared__ unsigned s_last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int group = p.q_heads / p.c.heads;
+  const uint32_t ring = smem_u32(smem) + warp * Sh::kStages * Sh::kStage;
+  const uint32_t bar = smem_u32(s_bar) + warp * Sh::kStages * 8;
+  if (lane < Sh::kStages) mbar_init(bar + 8 * lane, 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  if (tid == 0) s_abort = 0;
+  pdl_wait();
+
+  // this CTA's run of the list of units: a prefix sum over the sequences
+  const int per = (p.batch + kKvAttnThreads - 1) / kKvAttnThreads;
+  int64_t mine = 0;
+  for (int b = tid * per; b < min(p.batch, (tid + 1) * per); ++b) {
+    const KvSpan v = kv_span<R>(p, b, group);
+    mine += (int64_t)v.rt * p.c.heads * v.units;
   }
-  if (h >= p.q_heads || !found) return;
-  const int hk = h / (p.q_heads / p.c.heads);
-  for (int d = lane; d < D; d += 32) sq[warp][d] = Dt<DT>::to_f(p.Q[row * p.q_ts + h * p.q_hs + d]) * p.scale;
-  __syncwarp();
-  const int pos = s.len - s.n + (row - s.q0);
-  const int hi = p.causal ? min(s.len, pos + 1) : s.len;
-  const int lo = p.window ? max(0, pos - p.window + 1) : 0;
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < kKvWarps; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  incl += before;
+  const int ctas = (int)min((int64_t)gridDim.x, (total + kKvMinUnits - 1) / kKvMinUnits);
+  const int c = blockIdx.x;
+  if (c >= ctas) return;
+  int64_t x = total * c / ctas;
+  const int64_t x_begin = x, x1 = total * (c + 1) / ctas;
+  if (x >= incl - mine && x < incl) s_first[0] = tid * per, s_first[1] = incl - mine;
+  __syncthreads();
+  int b = (int)s_first[0];
+  int64_t base = s_first[1];
+  KvSpan v = kv_span<R>(p, b, group);
   const int64_t pages = p.c.slots >> p.c.page_log2;
-  auto vec_of = [&](int j) -> int64_t {
-    const int pg = kv_page(p, b, j >> p.c.page_log2, pages);
-    return pg < 0 ? -1 : ((((int64_t)pg * p.c.heads + hk) << p.c.page_log2) + (j & ((1 << p.c.page_log2) - 1)));
-  };
-  auto value = [&](int which, int64_t vec, int d) -> float {
-    const int blk = d / B, i = (d % B) / 8;
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(p.c.codes[which]) + vec * W + i * NB + blk);
-    const uint32_t st = __ldg(p.c.state[which] + vec * NB + blk);
-    return __half2float(__ushort_as_half((unsigned short)(st & 0xFFFFu))) *
-           ((float)((w >> (4 * (d & 7))) & 15u) - __half2float(__ushort_as_half((unsigned short)(st >> 16))));
-  };
-  float m = -INFINITY, l = 0.0f;
-  float o[D / 32] = {};
-  for (int j0 = lo; j0 < hi; j0 += 32) {
-    const int j = j0 + lane;
-    const int64_t vec = j < hi ? vec_of(j) : -1;
-    float x = -INFINITY;
-    if (vec >= 0) {
-      x = 0.0f;
-      for (int d = 0; d < D; ++d) x = fmaf(sq[warp][d], value(0, vec, d), x);
+  const int page_mask = (1 << p.c.page_log2) - 1;
+  constexpr float kLog2e = 1.4426950408889634f;
+  uint32_t seq_no = 0;  // stages this warp has used
+
+  while (x < x1) {
+    while (x >= base + (int64_t)v.rt * p.c.heads * v.units) {
+      base += (int64_t)v.rt * p.c.heads * v.units;
+      v = kv_span<R>(p, ++b, group);
     }
-    float mx = x;
-    for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-    const float mn = fmaxf(m, mx);
-    const float ref = mn == -INFINITY ? 0.0f : mn;
-    const float f = __expf(m - ref), pr = expf(x - ref);
-    float sum = pr;
-    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    l = l * f + sum;
-    for (int e = 0; e < D / 32; ++e) o[e] *= f;
-    m = mn;
-    for (int k = 0; k < 32 && j0 + k < hi; ++k) {
-      const int64_t vk = __shfl_sync(0xffffffffu, vec, k);
-      const float pk = __shfl_sync(0xffffffffu, pr, k);
-      if (vk >= 0)
-        for (int e = 0; e < D / 32; ++e) o[e] = fmaf(pk, value(1, vk, lane + 32 * e), o[e]);
+    const int seg = (int)((x - base) / v.units);  // row tile and kv head, heads fastest
+    const int first = (int)((x - base) - (int64_t)seg * v.units);
+    const int count = (int)min((int64_t)(v.units - first), x1 - x);
+    const int r0 = seg / p.c.heads * R, hk = seg % p.c.heads;
+    const int rows = min(R, v.s.n * group - r0);
+    // keys that some and that all rows of the tile attend to
+    const int i0 = r0 / group, i1 = (r0 + rows - 1) / group, p0 = v.s.len - v.s.n;
+    auto hi_of = [&](int i) { return p.causal ? min(v.s.len, p0 + i + 1) : v.s.len; };
+    auto lo_of = [&](int i) { return p.window ? max(0, p0 + i - p.window + 1) : 0; };
+    const int hi_all = hi_of(i0), hi_any = hi_of(i1), lo_all = lo_of(i1), lo_any = lo_of(i0);
+
+    // copies of unit first + k into stage k & 1: lane 4 part + kind copies
+    // (codes or states of K or V) a page's part
+    constexpr int kMaxParts = 2;
+    const int part_log2 = min(p.c.page_log2, 5);  // keys of a part: a page's, at most a unit's
+    auto page_of = [&](int k) -> int {  // page of this lane's part, -1 to leave it out
+      const int part = lane >> 2;
+      const int key = (v.u0 + first + k) * kKvUnit + (part << part_log2);
+      // parts outside what any row attends to may have no page: left out
+      if (k >= count || part >= kMaxParts >> (part_log2 == 5 ? 1 : 0) || key >= hi_any || key + (1 << part_log2) <= lo_any)
+        return -1;
+      return kv_page(p, b, key >> p.c.page_log2, pages);
+    };
+    uint32_t there = 0;  // bit stage * 2 + part: the part was copied
+    auto issue = [&](int k, int pg, uint32_t no) {
+      const int st = no % Sh::kStages, part = lane >> 2, kind = lane & 3, which = kind & 1;
+      const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0);
+      there = (there & ~(3u << (2 * st))) | (((ok & 1u) | ((ok >> 3) & 2u)) << (2 * st));
+      const uint32_t parts = __popc(ok & 0x11u), keys = 1u << part_log2;
+      if (lane == 0) mbar_arrive_expect_tx(bar + 8 * st, parts * 2 * keys * (D / 2 + NB * 4));
+      __syncwarp();
+      if (pg >= 0) {
+        const int key = (v.u0 + first + k) * kKvUnit + (part << part_log2);
+        const int64_t vec = ((((int64_t)pg * p.c.heads + hk) << p.c.page_log2) + (key & page_mask));
+        const uint32_t dst = ring + st * Sh::kStage + which * (Sh::kCodes + Sh::kState);
+        if (kind < 2) kv_bulk_load(dst + part * keys * (D / 2), p.c.codes[which] + vec * (D / 2), keys * (D / 2), bar + 8 * st);
+        else kv_bulk_load(dst + Sh::kCodes + part * keys * NB * 4, p.c.state[which] + vec * NB, keys * NB * 4, bar + 8 * st);
+      }
+    };
+    // this warp's units: first + warp, + 8, ...
+    int k_issue = warp;
+#pragma unroll
+    for (int s = 0; s < Sh::kStages; ++s) {
+      if (k_issue < count) issue(k_issue, page_of(k_issue), seq_no + s);
+      k_issue += kKvWarps;
     }
+    int pg_next = page_of(k_issue);
+
+    // the query rows, scaled into binary16, in the order of the words, and
+    // their sums
+    for (int r = warp; r < R; r += kKvWarps) {
+      const int row = r0 + r, i = row / group, h = hk * group + row % group;
+      const bool real = r < rows;
+      const uint16_t *q = p.Q + (int64_t)(v.s.q0 + i) * p.q_ts + (int64_t)h * p.q_hs;
+      // lane: word `lane` of D / 8 (the upper lanes idle for D = 64 and 128: 8 or 16 words)
+      float f[8];
+      float top = 0.0f;
+      const int wj = lane % NB, wi = lane / NB;
+      uint4 raw = make_uint4(0, 0, 0, 0);
+      if (real && lane < D / 8) raw = __ldcg(reinterpret_cast<const uint4 *>(q + wj * B + 8 * wi));
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[2 * e] = lo16<DT>(w[e]), f[2 * e + 1] = hi16<DT>(w[e]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int ex = top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127, -110) : 0;
+      const float up = __uint_as_float((uint32_t)min(127 + 14 - ex, 254) << 23);  // 2^(14 - ex)
+      float sum = 0.0f;
+      __half hq[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // nibbles 1, 3, 5, 7 of a word are read 16 times their code
+        hq[e] = __float2half_rn(f[e] * up);
+        sum += __half2float(hq[e]);
+        if (e & 1) hq[e] = __float2half_rn(f[e] * up * 0.0625f);
+      }
+      if (lane < D / 8) {
+        auto pk = [&](int a, int b2) { return (uint32_t)__half_as_ushort(hq[a]) | ((uint32_t)__half_as_ushort(hq[b2]) << 16); };
+        *reinterpret_cast<uint4 *>(s_q + r * Sh::kQRow + lane * 16) = make_uint4(pk(0, 4), pk(1, 5), pk(2, 6), pk(3, 7));
+      }
+      const float hf = ldexpf(p.scale * kLog2e, 24 - 14 + ex);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        float s = lane < D / 8 && wj == j ? sum : 0.0f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) s_qs[j][r] = s * ldexpf(p.scale * kLog2e, ex - 14);
+      }
+      if (lane == 0) s_hf[r] = hf;
+    }
+    __syncthreads();
+
+    float o_acc[NT][MT][4], m_run[NT][2], l_run[NT][2], zs[NT][NB][2], hf[NT][2], qs[NT][NB][2];
+    int hi[NT][2], lo[NT][2];
+    uint32_t qf[NT == 1 ? W4 : 1][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * t + e;
+        hf[n][e] = s_hf[r];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) qs[n][j][e] = s_qs[j][r], zs[n][j][e] = 0.0f;
+        m_run[n][e] = -INFINITY, l_run[n][e] = 0.0f;
+        const int i = (r0 + r) / group;
+        hi[n][e] = hi_of(i), lo[n][e] = lo_of(i);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o_acc[n][m][e] = 0.0f;
+    }
+    if constexpr (NT == 1) {
+#pragma unroll
+      for (int w = 0; w < W4; ++w) {
+        const uint4 q4v = *reinterpret_cast<const uint4 *>(s_q + g * Sh::kQRow + (W4 * t + w) * 16);
+        qf[w][0] = q4v.x, qf[w][1] = q4v.y, qf[w][2] = q4v.z, qf[w][3] = q4v.w;
+      }
+    }
+
+    for (int k = warp; k < count; k += kKvWarps, ++seq_no) {
+      const int st = seq_no % Sh::kStages;
+      if (!mbar_wait_warp(bar + 8 * st, (seq_no / Sh::kStages) & 1, p.status, &s_abort, p.wait_ns)) break;
+      const uint8_t *kc = smem + (ring - smem_u32(smem)) + st * Sh::kStage;
+      const uint32_t *ks = reinterpret_cast<const uint32_t *>(kc + Sh::kCodes);
+      const uint8_t *vc = kc + Sh::kCodes + Sh::kState;
+      const uint32_t *vs = reinterpret_cast<const uint32_t *>(vc + Sh::kCodes);
+      const int key0 = (v.u0 + first + k) * kKvUnit;
+      const uint32_t parts = (there >> (2 * st)) & 3u;
+      const bool inside = key0 >= lo_all && key0 + kKvUnit <= hi_all && (parts == 3u || (parts == 1u && part_log2 == 5));
+      // a key can be read: inside the lengths and its page was there
+      auto real_key = [&](int kk) {
+        return key0 + kk < hi_any && key0 + kk >= lo_any && ((parts >> (kk >> part_log2)) & 1u);
+      };
+      float sv[2][2][NB], zv[2][2][NB];  // [16-key tile][row g, g + 8][block]
+      float xs[2][NT][4], m_new[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) m_new[n][0] = m_new[n][1] = -INFINITY;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        float acc[NT][NB][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.0f;
+        uint32_t wa[W4], wb[W4];
+        const uint8_t *ra = kc + (16 * mt + g) * (D / 2) + t * (W4 * 4);
+        if constexpr (W4 == 4) {
+          const uint4 a = *reinterpret_cast<const uint4 *>(ra), bb = *reinterpret_cast<const uint4 *>(ra + 8 * (D / 2));
+          wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w;
+          wb[0] = bb.x, wb[1] = bb.y, wb[2] = bb.z, wb[3] = bb.w;
+        } else {
+          const uint2 a = *reinterpret_cast<const uint2 *>(ra), bb = *reinterpret_cast<const uint2 *>(ra + 8 * (D / 2));
+          wa[0] = a.x, wa[1] = a.y;
+          wb[0] = bb.x, wb[1] = bb.y;
+        }
+#pragma unroll
+        for (int w = 0; w < W4; ++w) {
+          const int j = w % NB;
+          const uint32_t a8 = wa[w] >> 8, b8 = wb[w] >> 8;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            uint32_t q0, q1, q2, q3;
+            if constexpr (NT == 1) {
+              q0 = qf[w][0], q1 = qf[w][1], q2 = qf[w][2], q3 = qf[w][3];
+            } else {
+              const uint4 q4v = *reinterpret_cast<const uint4 *>(s_q + (8 * n + g) * Sh::kQRow + (W4 * t + w) * 16);
+              q0 = q4v.x, q1 = q4v.y, q2 = q4v.z, q3 = q4v.w;
+            }
+            mma_f16(acc[n][j], wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u, wb[w] & 0x00F000F0u, q0, q1);
+            mma_f16(acc[n][j], a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, q2, q3);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int kk = 16 * mt + g + 8 * h;
+          const bool ok = inside || real_key(kk);
+          float sk[NB], sz[NB], top = 0.0f;
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            const uint32_t a = ok ? ks[kk * NB + j] : 0u, c2 = ok ? vs[kk * NB + j] : 0u;
+            sk[j] = half_lo(a);
+            sz[j] = sk[j] * half_hi(a);
+            sv[mt][h][j] = half_lo(c2);
+            zv[mt][h][j] = half_hi(c2);
+            top = fmaxf(top, sv[mt][h][j]);
+          }
+          const float ev = (float)max((int)(__float_as_uint(top) >> 23) - 127, -24);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float s = 0.0f;
+#pragma unroll
+              for (int j = 0; j < NB; ++j) s += sk[j] * (acc[n][j][2 * h + e] * hf[n][e]) - sz[j] * qs[n][j][e];
+              if (!inside && (!ok || key0 + kk >= hi[n][e] || key0 + kk < lo[n][e])) s = -INFINITY;
+              xs[mt][n][2 * h + e] = s;
+              m_new[n][e] = fmaxf(m_new[n][e], s + ev);
+            }
+        }
+      }
+      bool grow = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) m_new[n][e] = fmaxf(m_new[n][e], __shfl_xor_sync(0xffffffffu, m_new[n][e], o));
+          grow |= m_new[n][e] > m_run[n][e] + kKvSlack;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+        // the maximum moves only when it grows by more than kKvSlack: the
+        // weights stay below 2^(kKvSlack + 1)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float to = fmaxf(m_run[n][e], m_new[n][e]);
+            const float f = m_run[n][e] == -INFINITY ? 0.0f : ex2(m_run[n][e] - to);
+            m_run[n][e] = to;
+            l_run[n][e] *= f;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) zs[n][j][e] *= f;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) o_acc[n][m][e] *= f, o_acc[n][m][2 + e] *= f;
+          }
+      }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t bw[NT][NB][2];  // the weights as B operand: key pairs of one query row
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float pr[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float m = m_run[n][i & 1];
+            pr[i] = ex2(xs[mt][n][i] - (m == -INFINITY ? 0.0f : m));
+            l_run[n][i & 1] += pr[i];
+          }
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // a masked weight is zero whatever the key's state holds
+              float w0 = pr[2 * h] * sv[mt][h][j], w1 = pr[2 * h + 1] * sv[mt][h][j];
+              if (!inside) {
+                if (xs[mt][n][2 * h] == -INFINITY) w0 = 0.0f;
+                if (xs[mt][n][2 * h + 1] == -INFINITY) w1 = 0.0f;
+              }
+              const uint32_t ww = Dt<Q4_F16>::pack2(w0, w1);
+              // the zero-points' part, with the weights as the MMAs see them
+              zs[n][j][0] = fmaf(half_lo(ww), zv[mt][h][j], zs[n][j][0]);
+              zs[n][j][1] = fmaf(half_hi(ww), zv[mt][h][j], zs[n][j][1]);
+              bw[n][j][h] = movmatrix(ww);
+            }
+        }
+        // values: keys 2t, 2t + 1, 2t + 8, 2t + 9 of the tile, this lane's words of each
+        constexpr int WS = D / 64;
+        uint32_t vw[4][WS];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t *r = vc + (16 * mt + 2 * t + (i & 1) + 8 * (i >> 1)) * (D / 2) + g * (WS * 4);
+          if constexpr (WS == 2) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(r);
+            vw[i][0] = u.x, vw[i][1] = u.y;
+          } else {
+            vw[i][0] = *reinterpret_cast<const uint32_t *>(r);
+          }
+        }
+#pragma unroll
+        for (int ws = 0; ws < WS; ++ws) {
+          const int j = ws % NB;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {  // elements 0..3, 4..7 of the words
+            const uint32_t sel = half ? 0x7632u : 0x5410u;
+            const uint32_t a = __byte_perm(vw[0][ws], vw[1][ws], sel), c2 = __byte_perm(vw[2][ws], vw[3][ws], sel);
+            const uint32_t a8 = a >> 8, c8 = c2 >> 8;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_f16(o_acc[n][4 * ws + 2 * half], a & 0x000F000Fu, a & 0x00F000F0u, c2 & 0x000F000Fu, c2 & 0x00F000F0u,
+                      bw[n][j][0], bw[n][j][1]);
+              mma_f16(o_acc[n][4 * ws + 2 * half + 1], a8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x000F000Fu,
+                      c8 & 0x00F000F0u, bw[n][j][0], bw[n][j][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();  // the stage has been read
+      const int next = k + Sh::kStages * kKvWarps;
+      if (next < count) issue(next, pg_next, seq_no + Sh::kStages);
+      pg_next = page_of(next + kKvWarps);
+    }
+
+    // ---- the warps join ----
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          l_run[n][e] += __shfl_xor_sync(0xffffffffu, l_run[n][e], o);
+#pragma unroll
+          for (int j = 0; j < NB; ++j) zs[n][j][e] += __shfl_xor_sync(0xffffffffu, zs[n][j][e], o);
+        }
+        if (g == 0) {
+          s_m[warp * R + 8 * n + 2 * t + e] = m_run[n][e];
+          s_l[warp * R + 8 * n + 2 * t + e] = l_run[n][e];
+        }
+      }
+    __syncthreads();
+    auto join_max = [&](int r) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kKvWarps; ++w) m = fmaxf(m, s_m[w * R + r]);
+      return m;
+    };
+    {
+      auto put = [&](bool add) {
+        float *o = s_o + (warp & 3) * R * Sh::kORow;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * n + 2 * t + e;
+            const float m = join_max(r);
+            const float f = m_run[n][e] == -INFINITY ? 0.0f : ex2(m_run[n][e] - m);
+#pragma unroll
+            for (int ws = 0; ws < D / 64; ++ws) {
+              const int j = ws % NB;
+              // word (D / 64) g + ws of the row: element 8 i of block j
+              const int word = (D / 64) * g + ws, d0 = (word % NB) * B + 8 * (word / NB);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                float2 val;
+                val.x = f * fmaf(o_acc[n][4 * ws + q][e], 16777216.0f, -zs[n][j][e]);
+                val.y = f * fmaf(o_acc[n][4 * ws + q][2 + e], 1048576.0f, -zs[n][j][e]);
+                float2 *dst = reinterpret_cast<float2 *>(o + r * Sh::kORow + d0 + 2 * q);
+                if (add) {
+                  const float2 old = *dst;
+                  val.x += old.x, val.y += old.y;
+                }
+                *dst = val;
+              }
+            }
+          }
+      };
+      if (warp >= 4) put(false);
+      __syncthreads();
+      if (warp < 4) put(true);
+      __syncthreads();
+    }
+    const bool whole = count == v.units;
+    const int64_t seg0 = base + (int64_t)seg * v.units;  // the segment's units in the list
+    auto owner = [&](int64_t u) { return (int)(((u + 1) * ctas - 1) / total); };
+    auto part_of = [&](int cta) { return p.parts + ((int64_t)cta * 2 + (total * cta / ctas < seg0 ? 1 : 0)) * Sh::kPart; };
+    // row r of the tile, elements d .. d + 3, from the sums o, the maximum and l
+    auto finish = [&](int r, int d, float4 o, float m, float l) {
+      if (r >= rows) return;
+      const int i = (r0 + r) / group, h = hk * group + (r0 + r) % group;
+      const int64_t at = (int64_t)(v.s.q0 + i) * p.q_heads + h;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      uint2 out;
+      out.x = Dt<DT>::pack2(o.x * inv, o.y * inv);
+      out.y = Dt<DT>::pack2(o.z * inv, o.w * inv);
+      *reinterpret_cast<uint2 *>(p.out + at * D + d) = out;
+      if (d == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+    };
+    for (int i = tid; i < R * D / 4; i += kKvAttnThreads) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
+      float4 o = *reinterpret_cast<const float4 *>(s_o + r * Sh::kORow + d);
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        const float4 a = *reinterpret_cast<const float4 *>(s_o + (w * R + r) * Sh::kORow + d);
+        o.x += a.x, o.y += a.y, o.z += a.z, o.w += a.w;
+      }
+      const float m = join_max(r);
+      float l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kKvWarps; ++w) {
+        const float mw = s_m[w * R + r];
+        l += s_l[w * R + r] * (mw == -INFINITY ? 0.0f : ex2(mw - m));  // 0 * NaN keeps a NaN
+      }
+      if (whole) {
+        finish(r, d, o, m, l);
+      } else {
+        float *part = part_of(c);
+        __stcg(reinterpret_cast<float4 *>(part + r * D + d), o);
+        if (d == 0) __stcg(reinterpret_cast<float2 *>(part + R * D) + r, make_float2(m, l));
+      }
+    }
+    if (!whole) {
+      // the CTAs of the segment join: counted on the first one's word
+      const int c0 = owner(seg0), c1 = owner(seg0 + v.units - 1);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const unsigned old = atomicAdd(p.counts + c0, 1u);
+        s_last = old == (unsigned)(c1 - c0);
+        if (s_last) p.counts[c0] = 0u;
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        for (int i = tid; i < R * D / 4; i += kKvAttnThreads) {
+          const int r = i / (D / 4), d = i % (D / 4) * 4;
+          float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          float m = -INFINITY, l = 0.0f;
+          constexpr int kAhead = 8;  // partial results on their way at once
+          for (int cc = c0; cc <= c1; cc += kAhead) {
+            float4 po[kAhead];
+            float2 ml[kAhead];
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+              const float *part = part_of(min(cc + a, c1));
+              po[a] = __ldcg(reinterpret_cast<const float4 *>(part + r * D + d));
+              ml[a] = __ldcg(reinterpret_cast<const float2 *>(part + R * D) + r);
+            }
+            float top = m;
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+              if (cc + a <= c1) top = fmaxf(top, ml[a].x);
+            const float f = m == -INFINITY ? 0.0f : ex2(m - top);
+            o.x *= f, o.y *= f, o.z *= f, o.w *= f, l *= f;
+            m = top;
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+              if (cc + a <= c1) {
+                const float fa = ml[a].x == -INFINITY ? 0.0f : ex2(ml[a].x - top);
+                o.x = fmaf(po[a].x, fa, o.x), o.y = fmaf(po[a].y, fa, o.y);
+                o.z = fmaf(po[a].z, fa, o.z), o.w = fmaf(po[a].w, fa, o.w);
+                l = fmaf(ml[a].y, fa, l);
+              }
+          }
+          finish(r, d, o, m, l);
+        }
+      }
+    }
+    __syncthreads();  // shared memory is free for the next segment
+    x += count;
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  for (int e = 0; e < D / 32; ++e)
-    p.out[((int64_t)row * p.q_heads + h) * D + lane + 32 * e] = Dt<DT>::from_f(l == 0.0f ? 0.0f : o[e] * inv);
-  if (p.lse && lane == 0) p.lse[(int64_t)row * p.q_heads + h] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) + logf(l);
+  if (s_abort) {
+    // after a timeout the copies that nobody waits for get a millisecond
+    // (they take microseconds) before the CTA ends
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+  }
 }
 
 }  // namespace q4

@@ -208,7 +208,7 @@ int q4_kv_attention_workspace_size(const q4_kv_cache *cache, int64_t batch, int6
   const int rc = check_cache(cache, &v);
   if (rc != Q4_OK) return rc;
   if (batch < 1 || batch > 65535 || total_q < 1 || total_q > kMaxRows || q_heads < 1 || q_heads % v.heads) return Q4_ERR_SHAPE;
-  *bytes = 0;
+  *bytes = kv_attention_ws(cache->head_dim, plan_sms());
   return Q4_OK;
 }
 
@@ -242,8 +242,11 @@ int q4_kv_attention(const q4_kv_cache *cache, const void *Q, int32_t dtype, int6
   p.window = (int32_t)std::min<int64_t>(window, INT32_MAX);
   p.out = (uint16_t *)out;
   p.lse = lse;
+  p.counts = (unsigned *)workspace;
+  p.parts = (float *)((char *)workspace + kKvCountBytes);
+  p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   p.status = di.status;
-  return run_kv_attention(dtype, cache->head_dim, cache->blocksize, p, (cudaStream_t)stream);
+  return run_kv_attention(dtype, cache->head_dim, cache->blocksize, p, max_q, di.sms, (cudaStream_t)stream);
 }
 
 }  // extern "C"

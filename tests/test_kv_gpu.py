@@ -165,7 +165,7 @@ def reference(c, table, lens, qs, q, scale, causal, window):
     is taken off: 30 |q| s each)."""
     D, heads = c.head_dim, c.kv_heads
     k_all, v_all = values(c.k_codes, c.k_state), values(c.v_codes, c.v_state)
-    ks = c.k_state[..., 0].cpu().double()
+    ks, vs = c.k_state[..., 0].cpu().double(), c.v_state[..., 0].cpu().double()
     group = q.shape[1] // heads
     q = q.cpu().double()
     out = torch.zeros(q.shape, dtype=torch.float64)
@@ -187,7 +187,7 @@ def reference(c, table, lens, qs, q, scale, causal, window):
             hk = h // group
             k = k_all[pg, hk].reshape(-1, D)[:length]
             v = v_all[pg, hk].reshape(-1, D)[:length]
-            s = ks[pg, hk].reshape(-1, ks.shape[-1])[:length].repeat_interleave(D // ks.shape[-1], 1)
+            s, sv = (x[pg, hk].reshape(-1, x.shape[-1])[:length].repeat_interleave(D // x.shape[-1], 1) for x in (ks, vs))
             qh = q[row:row + n, h]
             x = (qh @ k.t() * scale).masked_fill(~seen, -math.inf)
             dx = abs(scale) * (2.0 ** -11 * (qh.abs() @ k.abs().t()) + (D + 2) * 2.0 ** -24 * (qh.abs() @ (30 * s).t()))
@@ -202,6 +202,9 @@ def reference(c, table, lens, qs, q, scale, causal, window):
             rel = 2 * torch.expm1(dx) + 2.0 ** -10 + 2.0 ** -20
             tiny = 2.0 ** -23 * length
             tol[row:row + n, h] = rel[:, None] * (p @ v.abs()) + tiny * p.amax(1, keepdim=True) * v.abs().amax(0)
+            # sum w code - sum w z, each up to 15 sum w s, where both are summed in binary32: a step of 2^-23 for each
+            # of length / 16 accumulations of 16 keys and of the joins of up to 32 partial sums
+            tol[row:row + n, h] += (length / 16 + 32) * 2.0 ** -23 * 15 * (p @ sv)
             ltol[row:row + n, h] = dx + 2.0 ** -22 * (m.abs().nan_to_num(posinf=0) + 1)
         row += n
     return out, lse, tol, ltol
