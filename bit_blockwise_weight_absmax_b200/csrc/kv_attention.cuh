@@ -75,8 +75,8 @@ __device__ __forceinline__ int kv_page(const KvAttnParams &p, int b, int i, int6
 
 constexpr int kKvUnit = 32;    // keys per unit
 constexpr int kKvWarps = 8;
-constexpr int kKvMinUnits = 8; // units a CTA takes at least: one for each warp
 constexpr float kKvSlack = 8.0f;
+constexpr float kKvMasked = -3.4028235e38f;  // in the place of a score that does not count
 constexpr int kKvAttnThreads = kKvWarps * 32;
 constexpr size_t kKvCountBytes = Q4_WORKSPACE_HEAD;
 
@@ -91,6 +91,17 @@ template <int D, int B, int NT> struct KvShape {
   static constexpr int kRing = kKvWarps * kStages * kStage;
   static constexpr int kSmem = kRing + R * kQRow + 4 * R * kORow * 4 + 2 * kKvWarps * R * 4;
   static constexpr int kPart = R * (D + 2);  // floats of a partial result: O, then M and l
+  static constexpr int kRowsPerWarp = (R + kKvWarps - 1) / kKvWarps;
+};
+
+// What a warp keeps of its query rows over a segment: columns 8 n + 2 t + e.
+template <int D, int B, int NT> struct KvRun {
+  static constexpr int NB = D / B;
+  float o[NT][D / 16][4];           // output^T: rows d, columns query rows
+  float m[NT][2], l[NT][2];         // running maximum, sum of weights over exponents
+  float zs[NT][NB][2];              // sum w z per block
+  float hf[NT][2], qs[NT][NB][2];   // score factor, the query's block sums
+  int hi[NT][2], lo[NT][2];         // keys the row attends to
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -109,6 +120,11 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float half_lo(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu))); }
@@ -136,11 +152,209 @@ template <int R> __device__ __forceinline__ KvSpan kv_span(const KvAttnParams &p
   return v;
 }
 
+// One unit: 32 keys whose codes and states lie in shared memory.  MASK: some
+// key is outside some row's range, or its page was not there.
+template <int D, int B, int NT, bool MASK>
+__device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc, const uint8_t *s_q, int key0, int lane,
+                                        int hi_any, int lo_any, uint32_t parts, int part_log2) {
+  using Sh = KvShape<D, B, NT>;
+  constexpr int NB = Sh::NB, W4 = D / 32, MT = D / 16;
+  const int g = lane >> 2, t = lane & 3;
+  const uint8_t *ks = kc + Sh::kCodes, *vc = ks + Sh::kState, *vs = vc + Sh::kCodes;
+  float sv[2][2][NB], zv[2][2][NB];  // [16-key tile][row g, g + 8][block]
+  float xs[2][NT][4];                // scores before the factor hf
+  float m_new[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) m_new[n][0] = m_new[n][1] = -INFINITY;
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    float acc[NT][NB][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.0f;
+    uint32_t wa[W4], wb[W4];
+    const uint8_t *ra = kc + (16 * mt + g) * (D / 2) + t * (W4 * 4);
+    if constexpr (W4 == 4) {
+      const uint4 a = *reinterpret_cast<const uint4 *>(ra), bb = *reinterpret_cast<const uint4 *>(ra + 8 * (D / 2));
+      wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w;
+      wb[0] = bb.x, wb[1] = bb.y, wb[2] = bb.z, wb[3] = bb.w;
+    } else {
+      const uint2 a = *reinterpret_cast<const uint2 *>(ra), bb = *reinterpret_cast<const uint2 *>(ra + 8 * (D / 2));
+      wa[0] = a.x, wa[1] = a.y;
+      wb[0] = bb.x, wb[1] = bb.y;
+    }
+#pragma unroll
+    for (int w = 0; w < W4; ++w) {
+      const int j = w % NB;
+      const uint32_t a8 = wa[w] >> 8, b8 = wb[w] >> 8;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(s_q + (8 * n + g) * Sh::kQRow + (W4 * t + w) * 16);
+        mma_f16(acc[n][j], wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u, wb[w] & 0x00F000F0u, q.x, q.y);
+        mma_f16(acc[n][j], a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, q.z, q.w);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int kk = 16 * mt + g + 8 * h;
+      // a key can be read: inside the lengths, and its page was there
+      const bool ok = !MASK || (key0 + kk < hi_any && key0 + kk >= lo_any && ((parts >> (kk >> part_log2)) & 1u));
+      uint32_t ka[NB], va[NB];
+      if constexpr (NB == 2) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(ks + kk * 8), w = *reinterpret_cast<const uint2 *>(vs + kk * 8);
+        ka[0] = u.x, ka[1] = u.y, va[0] = w.x, va[1] = w.y;
+      } else {
+        ka[0] = *reinterpret_cast<const uint32_t *>(ks + kk * 4), va[0] = *reinterpret_cast<const uint32_t *>(vs + kk * 4);
+      }
+      float sk[NB], sz[NB], top = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        if (!ok) ka[j] = va[j] = 0u;
+        sk[j] = half_lo(ka[j]);
+        sz[j] = sk[j] * half_hi(ka[j]);
+        sv[mt][h][j] = half_lo(va[j]);
+        zv[mt][h][j] = half_hi(va[j]);
+        top = fmaxf(top, sv[mt][h][j]);
+      }
+      const float ev = fmaxf(lg2(top), -24.0f);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float s = sk[0] * acc[n][0][2 * h + e];
+          if constexpr (NB == 2) s = fmaf(sk[1], acc[n][1][2 * h + e], s);
+#pragma unroll
+          for (int j = 0; j < NB; ++j) s = fmaf(-sz[j], run.qs[n][j][e], s);
+          float x = fmaf(s, run.hf[n][e], ev);
+          if (MASK && (!ok || key0 + kk >= run.hi[n][e] || key0 + kk < run.lo[n][e])) x = -INFINITY, s = kKvMasked;
+          xs[mt][n][2 * h + e] = s;
+          m_new[n][e] = fmaxf(m_new[n][e], x);
+        }
+    }
+  }
+  bool grow = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) m_new[n][e] = fmaxf(m_new[n][e], __shfl_xor_sync(0xffffffffu, m_new[n][e], o));
+      grow |= m_new[n][e] > run.m[n][e] + kKvSlack;
+    }
+  if (__any_sync(0xffffffffu, grow)) {
+    // the maximum moves only when it grows by more than kKvSlack: the weights
+    // stay below 2^(kKvSlack + 1)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float to = fmaxf(run.m[n][e], m_new[n][e]);
+        const float f = run.m[n][e] == -INFINITY ? 0.0f : ex2(run.m[n][e] - to);
+        run.m[n][e] = to;
+        run.l[n][e] *= f;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) run.zs[n][j][e] *= f;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) run.o[n][m][e] *= f, run.o[n][m][2 + e] *= f;
+      }
+  }
+  float mm[NT][2];  // minus the maximum
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mm[n][e] = run.m[n][e] == -INFINITY ? 0.0f : -run.m[n][e];
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+    uint32_t bw[NT][NB][2];  // the weights as B operand: key pairs of one query row
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float pr[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float s = xs[mt][n][2 * h + e];
+          pr[e] = ex2(fmaf(s, run.hf[n][e], mm[n][e]));
+          if (MASK && s == kKvMasked) pr[e] = 0.0f;
+          run.l[n][e] += pr[e];
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          float w0 = pr[0] * sv[mt][h][j], w1 = pr[1] * sv[mt][h][j];
+          if (MASK) {  // a masked weight is zero whatever the key's state holds
+            if (xs[mt][n][2 * h] == kKvMasked) w0 = 0.0f;
+            if (xs[mt][n][2 * h + 1] == kKvMasked) w1 = 0.0f;
+          }
+          const uint32_t ww = Dt<Q4_F16>::pack2(w0, w1);
+          // the zero-points' part, with the weights as the MMAs see them
+          run.zs[n][j][0] = fmaf(half_lo(ww), zv[mt][h][j], run.zs[n][j][0]);
+          run.zs[n][j][1] = fmaf(half_hi(ww), zv[mt][h][j], run.zs[n][j][1]);
+          bw[n][j][h] = movmatrix(ww);
+        }
+      }
+    // values: keys 2t, 2t + 1, 2t + 8, 2t + 9 of the tile, this lane's words of each
+    constexpr int WS = D / 64;
+    uint32_t vw[4][WS];
+    const uint8_t *rv = vc + (16 * mt + 2 * t) * (D / 2) + g * (WS * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t *r = rv + ((i & 1) + 8 * (i >> 1)) * (D / 2);
+      if constexpr (WS == 2) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(r);
+        vw[i][0] = u.x, vw[i][1] = u.y;
+      } else {
+        vw[i][0] = *reinterpret_cast<const uint32_t *>(r);
+      }
+    }
+#pragma unroll
+    for (int ws = 0; ws < WS; ++ws) {
+      const int j = ws % NB;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {  // elements 0..3, 4..7 of the words
+        const uint32_t sel = half ? 0x7632u : 0x5410u;
+        const uint32_t a = __byte_perm(vw[0][ws], vw[1][ws], sel), c = __byte_perm(vw[2][ws], vw[3][ws], sel);
+        const uint32_t a8 = a >> 8, c8 = c >> 8;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_f16(run.o[n][4 * ws + 2 * half], a & 0x000F000Fu, a & 0x00F000F0u, c & 0x000F000Fu, c & 0x00F000F0u,
+                  bw[n][j][0], bw[n][j][1]);
+          mma_f16(run.o[n][4 * ws + 2 * half + 1], a8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x000F000Fu, c8 & 0x00F000F0u,
+                  bw[n][j][0], bw[n][j][1]);
+        }
+      }
+    }
+  }
+}
+
+// A run of units of one segment: a row tile of a sequence and a kv head.
+template <int R> struct KvSegment {
+  KvSpan v;
+  int64_t base;            // the sequence's first unit in the list
+  int b, seg, first, count;
+  int r0, hk, rows;
+  int hi_all, hi_any, lo_all, lo_any;  // keys that all and that some rows of the tile attend to
+  __device__ __forceinline__ void ranges(const KvAttnParams &p, int group) {
+    r0 = seg / p.c.heads * R, hk = seg % p.c.heads;
+    rows = min(R, v.s.n * group - r0);
+    const int i0 = r0 / group, i1 = (r0 + rows - 1) / group;
+    hi_all = hi(p, i0), hi_any = hi(p, i1), lo_all = lo(p, i1), lo_any = lo(p, i0);
+  }
+  __device__ __forceinline__ int hi(const KvAttnParams &p, int i) const {
+    return p.causal ? min(v.s.len, v.s.len - v.s.n + i + 1) : v.s.len;
+  }
+  __device__ __forceinline__ int lo(const KvAttnParams &p, int i) const {
+    return p.window ? max(0, v.s.len - v.s.n + i - p.window + 1) : 0;
+  }
+};
+
 template <int DT, int D, int B, int NT>
 __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_attention_kernel(const __grid_constant__ KvAttnParams p) {
   using Sh = KvShape<D, B, NT>;
-  constexpr int NB = Sh::NB, R = Sh::R, W4 = D / 32;  // W4: words of a key a lane takes
-  constexpr int MT = D / 16;                          // 16-row tiles of the output's d
+  constexpr int NB = Sh::NB, R = Sh::R;
+  constexpr int MT = D / 16;  // 16-row tiles of the output's d
   pdl_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *s_q = smem + Sh::kRing;
@@ -148,13 +362,14 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   float *s_m = s_o + 4 * R * Sh::kORow, *s_l = s_m + kKvWarps * R;
   __shared__ uint64_t s_bar[kKvWarps * Sh::kStages];
   __shared__ float s_hf[R], s_qs[NB][R];
-  __shared__ int64_t s_scan[kKvWarps + 1], s_first[2];
-  __shared__ int s_abort;
+  __shared__ int64_t s_scan[kKvWarps], s_first[2];
+  __shared__ int s_segs[kKvWarps], s_abort;
   __shared__ unsigned s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int group = p.q_heads / p.c.heads;
-  const uint32_t ring = smem_u32(smem) + warp * Sh::kStages * Sh::kStage;
+  const uint8_t *ring = smem + warp * Sh::kStages * Sh::kStage;
+  const uint32_t ring_u = smem_u32(ring);
   const uint32_t bar = smem_u32(s_bar) + warp * Sh::kStages * 8;
   if (lane < Sh::kStages) mbar_init(bar + 8 * lane, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -164,9 +379,11 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   // this CTA's run of the list of units: a prefix sum over the sequences
   const int per = (p.batch + kKvAttnThreads - 1) / kKvAttnThreads;
   int64_t mine = 0;
+  int segs = 0;
   for (int b = tid * per; b < min(p.batch, (tid + 1) * per); ++b) {
     const KvSpan v = kv_span<R>(p, b, group);
     mine += (int64_t)v.rt * p.c.heads * v.units;
+    segs += min(v.rt, 1 << 16) * p.c.heads;
   }
   int64_t incl = mine;
 #pragma unroll
@@ -174,95 +391,108 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
     const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += u;
   }
-  if (lane == 31) s_scan[warp] = incl;
+  segs = min(segs, 1 << 20);
+  segs = __reduce_add_sync(0xffffffffu, segs);
+  if (lane == 31) s_scan[warp] = incl, s_segs[warp] = min(segs, 1 << 20);
   __syncthreads();
   int64_t before = 0, total = 0;
+  segs = 0;
   for (int w = 0; w < kKvWarps; ++w) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
+    segs += s_segs[w];
   }
   incl += before;
-  const int ctas = (int)min((int64_t)gridDim.x, (total + kKvMinUnits - 1) / kKvMinUnits);
+  if (total == 0) return;
+  // all CTAs, or where that leaves less than a unit for each warp, fewer; a
+  // multiple of the segments where there are few: equal ones are then cut
+  // alike, and none lies in two pieces of one CTA
+  int ctas = (int)min((int64_t)gridDim.x, (total + kKvWarps - 1) / kKvWarps);
+  if (segs <= (int)gridDim.x) ctas = segs * (int)min((int64_t)(gridDim.x / segs), (total + kKvWarps * segs - 1) / (kKvWarps * segs));
   const int c = blockIdx.x;
   if (c >= ctas) return;
   int64_t x = total * c / ctas;
-  const int64_t x_begin = x, x1 = total * (c + 1) / ctas;
+  const int64_t x1 = total * (c + 1) / ctas;
   if (x >= incl - mine && x < incl) s_first[0] = tid * per, s_first[1] = incl - mine;
   __syncthreads();
-  int b = (int)s_first[0];
-  int64_t base = s_first[1];
-  KvSpan v = kv_span<R>(p, b, group);
   const int64_t pages = p.c.slots >> p.c.page_log2;
   const int page_mask = (1 << p.c.page_log2) - 1;
+  const int part_log2 = min(p.c.page_log2, 5);  // keys of a part: a page's, at most a unit's
   constexpr float kLog2e = 1.4426950408889634f;
+
+  KvSegment<R> sg;
+  sg.b = (int)s_first[0];
+  sg.base = s_first[1];
+  sg.v = kv_span<R>(p, sg.b, group);
+  auto locate = [&] {  // sg: the segment of unit x, as far as this CTA takes it
+    while (x >= sg.base + (int64_t)sg.v.rt * p.c.heads * sg.v.units) {
+      sg.base += (int64_t)sg.v.rt * p.c.heads * sg.v.units;
+      sg.v = kv_span<R>(p, ++sg.b, group);
+    }
+    sg.seg = (int)((x - sg.base) / sg.v.units);
+    sg.first = (int)((x - sg.base) - (int64_t)sg.seg * sg.v.units);
+    sg.count = (int)min((int64_t)(sg.v.units - sg.first), x1 - x);
+    sg.ranges(p, group);
+  };
+  // copies of unit first + k: lane 4 part + kind copies (codes or states of K
+  // or V) a page's part
+  auto page_of = [&](int k) -> int {  // page of this lane's part, -1 to leave it out
+    const int part = lane >> 2;
+    const int key = (sg.v.u0 + sg.first + k) * kKvUnit + (part << part_log2);
+    // parts outside what any row attends to may have no page: left out
+    if (k >= sg.count || part >= (32 >> part_log2) || key >= sg.hi_any || key + (1 << part_log2) <= sg.lo_any) return -1;
+    return kv_page(p, sg.b, key >> p.c.page_log2, pages);
+  };
+  uint32_t there = 0;  // bit stage * 2 + part: the part was copied
+  auto issue = [&](int k, int pg, uint32_t no) {
+    const int st = no % Sh::kStages, part = lane >> 2, kind = lane & 3, which = kind & 1;
+    const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0);
+    there = (there & ~(3u << (2 * st))) | (((ok & 1u) | ((ok >> 3) & 2u)) << (2 * st));
+    const uint32_t parts = __popc(ok & 0x11u), keys = 1u << part_log2;
+    if (lane == 0) mbar_arrive_expect_tx(bar + 8 * st, parts * 2 * keys * (D / 2 + NB * 4));
+    __syncwarp();
+    if (pg >= 0) {
+      const int key = (sg.v.u0 + sg.first + k) * kKvUnit + (part << part_log2);
+      const int64_t vec = ((((int64_t)pg * p.c.heads + sg.hk) << p.c.page_log2) + (key & page_mask));
+      const uint32_t dst = ring_u + st * Sh::kStage + which * (Sh::kCodes + Sh::kState);
+      if (kind < 2) kv_bulk_load(dst + part * keys * (D / 2), p.c.codes[which] + vec * (D / 2), keys * (D / 2), bar + 8 * st);
+      else kv_bulk_load(dst + Sh::kCodes + part * keys * NB * 4, p.c.state[which] + vec * NB, keys * NB * 4, bar + 8 * st);
+    }
+  };
   uint32_t seq_no = 0;  // stages this warp has used
-
-  while (x < x1) {
-    while (x >= base + (int64_t)v.rt * p.c.heads * v.units) {
-      base += (int64_t)v.rt * p.c.heads * v.units;
-      v = kv_span<R>(p, ++b, group);
-    }
-    const int seg = (int)((x - base) / v.units);  // row tile and kv head, heads fastest
-    const int first = (int)((x - base) - (int64_t)seg * v.units);
-    const int count = (int)min((int64_t)(v.units - first), x1 - x);
-    const int r0 = seg / p.c.heads * R, hk = seg % p.c.heads;
-    const int rows = min(R, v.s.n * group - r0);
-    // keys that some and that all rows of the tile attend to
-    const int i0 = r0 / group, i1 = (r0 + rows - 1) / group, p0 = v.s.len - v.s.n;
-    auto hi_of = [&](int i) { return p.causal ? min(v.s.len, p0 + i + 1) : v.s.len; };
-    auto lo_of = [&](int i) { return p.window ? max(0, p0 + i - p.window + 1) : 0; };
-    const int hi_all = hi_of(i0), hi_any = hi_of(i1), lo_all = lo_of(i1), lo_any = lo_of(i0);
-
-    // copies of unit first + k into stage k & 1: lane 4 part + kind copies
-    // (codes or states of K or V) a page's part
-    constexpr int kMaxParts = 2;
-    const int part_log2 = min(p.c.page_log2, 5);  // keys of a part: a page's, at most a unit's
-    auto page_of = [&](int k) -> int {  // page of this lane's part, -1 to leave it out
-      const int part = lane >> 2;
-      const int key = (v.u0 + first + k) * kKvUnit + (part << part_log2);
-      // parts outside what any row attends to may have no page: left out
-      if (k >= count || part >= kMaxParts >> (part_log2 == 5 ? 1 : 0) || key >= hi_any || key + (1 << part_log2) <= lo_any)
-        return -1;
-      return kv_page(p, b, key >> p.c.page_log2, pages);
-    };
-    uint32_t there = 0;  // bit stage * 2 + part: the part was copied
-    auto issue = [&](int k, int pg, uint32_t no) {
-      const int st = no % Sh::kStages, part = lane >> 2, kind = lane & 3, which = kind & 1;
-      const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0);
-      there = (there & ~(3u << (2 * st))) | (((ok & 1u) | ((ok >> 3) & 2u)) << (2 * st));
-      const uint32_t parts = __popc(ok & 0x11u), keys = 1u << part_log2;
-      if (lane == 0) mbar_arrive_expect_tx(bar + 8 * st, parts * 2 * keys * (D / 2 + NB * 4));
-      __syncwarp();
-      if (pg >= 0) {
-        const int key = (v.u0 + first + k) * kKvUnit + (part << part_log2);
-        const int64_t vec = ((((int64_t)pg * p.c.heads + hk) << p.c.page_log2) + (key & page_mask));
-        const uint32_t dst = ring + st * Sh::kStage + which * (Sh::kCodes + Sh::kState);
-        if (kind < 2) kv_bulk_load(dst + part * keys * (D / 2), p.c.codes[which] + vec * (D / 2), keys * (D / 2), bar + 8 * st);
-        else kv_bulk_load(dst + Sh::kCodes + part * keys * NB * 4, p.c.state[which] + vec * NB, keys * NB * 4, bar + 8 * st);
-      }
-    };
-    // this warp's units: first + warp, + 8, ...
-    int k_issue = warp;
+  int pg_next = -1;
+  uint4 q_raw[Sh::kRowsPerWarp];
+  // the first units' copies and the query rows of a segment are on their way
+  // before the previous one's results are joined
+  const int wj = lane % NB, wi = lane / NB;  // the word of a query row this lane prepares
+  auto begin = [&] {
+    int pg[Sh::kStages];
 #pragma unroll
-    for (int s = 0; s < Sh::kStages; ++s) {
-      if (k_issue < count) issue(k_issue, page_of(k_issue), seq_no + s);
-      k_issue += kKvWarps;
+    for (int s = 0; s < Sh::kStages; ++s) pg[s] = page_of(warp + s * kKvWarps);
+    pg_next = page_of(warp + Sh::kStages * kKvWarps);
+#pragma unroll
+    for (int i = 0; i < Sh::kRowsPerWarp; ++i) {
+      const int r = warp + i * kKvWarps, row = sg.r0 + r;
+      q_raw[i] = make_uint4(0, 0, 0, 0);
+      if (r < sg.rows && lane < D / 8)
+        q_raw[i] = __ldcg(reinterpret_cast<const uint4 *>(p.Q + (int64_t)(sg.v.s.q0 + row / group) * p.q_ts +
+                                                          (int64_t)(sg.hk * group + row % group) * p.q_hs + wj * B + 8 * wi));
     }
-    int pg_next = page_of(k_issue);
+#pragma unroll
+    for (int s = 0; s < Sh::kStages; ++s)
+      if (warp + s * kKvWarps < sg.count) issue(warp + s * kKvWarps, pg[s], seq_no + s);
+  };
+  locate();
+  begin();
 
+  while (true) {
     // the query rows, scaled into binary16, in the order of the words, and
     // their sums
-    for (int r = warp; r < R; r += kKvWarps) {
-      const int row = r0 + r, i = row / group, h = hk * group + row % group;
-      const bool real = r < rows;
-      const uint16_t *q = p.Q + (int64_t)(v.s.q0 + i) * p.q_ts + (int64_t)h * p.q_hs;
-      // lane: word `lane` of D / 8 (the upper lanes idle for D = 64 and 128: 8 or 16 words)
-      float f[8];
-      float top = 0.0f;
-      const int wj = lane % NB, wi = lane / NB;
-      uint4 raw = make_uint4(0, 0, 0, 0);
-      if (real && lane < D / 8) raw = __ldcg(reinterpret_cast<const uint4 *>(q + wj * B + 8 * wi));
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < Sh::kRowsPerWarp; ++i) {
+      const int r = warp + i * kKvWarps;
+      const uint32_t w[4] = {q_raw[i].x, q_raw[i].y, q_raw[i].z, q_raw[i].w};
+      float f[8], top = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) f[2 * e] = lo16<DT>(w[e]), f[2 * e + 1] = hi16<DT>(w[e]);
 #pragma unroll
@@ -270,7 +500,7 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
 #pragma unroll
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int ex = top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127, -110) : 0;
-      const float up = __uint_as_float((uint32_t)min(127 + 14 - ex, 254) << 23);  // 2^(14 - ex)
+      const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);  // 2^(14 - ex)
       float sum = 0.0f;
       __half hq[8];
 #pragma unroll
@@ -284,219 +514,59 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
         auto pk = [&](int a, int b2) { return (uint32_t)__half_as_ushort(hq[a]) | ((uint32_t)__half_as_ushort(hq[b2]) << 16); };
         *reinterpret_cast<uint4 *>(s_q + r * Sh::kQRow + lane * 16) = make_uint4(pk(0, 4), pk(1, 5), pk(2, 6), pk(3, 7));
       }
-      const float hf = ldexpf(p.scale * kLog2e, 24 - 14 + ex);
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         float s = lane < D / 8 && wj == j ? sum : 0.0f;
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) s_qs[j][r] = s * ldexpf(p.scale * kLog2e, ex - 14);
+        if (lane == 0) s_qs[j][r] = s * 5.9604644775390625e-08f;  // 2^-24, as the codes
       }
-      if (lane == 0) s_hf[r] = hf;
+      if (lane == 0) s_hf[r] = ldexpf(p.scale * kLog2e, 24 - 14 + ex);
     }
     __syncthreads();
 
-    float o_acc[NT][MT][4], m_run[NT][2], l_run[NT][2], zs[NT][NB][2], hf[NT][2], qs[NT][NB][2];
-    int hi[NT][2], lo[NT][2];
-    uint32_t qf[NT == 1 ? W4 : 1][4];
+    KvRun<D, B, NT> run;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * n + 2 * t + e;
-        hf[n][e] = s_hf[r];
+        run.hf[n][e] = s_hf[r];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) qs[n][j][e] = s_qs[j][r], zs[n][j][e] = 0.0f;
-        m_run[n][e] = -INFINITY, l_run[n][e] = 0.0f;
-        const int i = (r0 + r) / group;
-        hi[n][e] = hi_of(i), lo[n][e] = lo_of(i);
+        for (int j = 0; j < NB; ++j) run.qs[n][j][e] = s_qs[j][r], run.zs[n][j][e] = 0.0f;
+        run.m[n][e] = -INFINITY, run.l[n][e] = 0.0f;
+        const int i = (sg.r0 + r) / group;
+        run.hi[n][e] = sg.hi(p, i), run.lo[n][e] = sg.lo(p, i);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o_acc[n][m][e] = 0.0f;
-    }
-    if constexpr (NT == 1) {
-#pragma unroll
-      for (int w = 0; w < W4; ++w) {
-        const uint4 q4v = *reinterpret_cast<const uint4 *>(s_q + g * Sh::kQRow + (W4 * t + w) * 16);
-        qf[w][0] = q4v.x, qf[w][1] = q4v.y, qf[w][2] = q4v.z, qf[w][3] = q4v.w;
-      }
+        for (int e = 0; e < 4; ++e) run.o[n][m][e] = 0.0f;
     }
 
-    for (int k = warp; k < count; k += kKvWarps, ++seq_no) {
+    for (int k = warp; k < sg.count; k += kKvWarps, ++seq_no) {
       const int st = seq_no % Sh::kStages;
       if (!mbar_wait_warp(bar + 8 * st, (seq_no / Sh::kStages) & 1, p.status, &s_abort, p.wait_ns)) break;
-      const uint8_t *kc = smem + (ring - smem_u32(smem)) + st * Sh::kStage;
-      const uint32_t *ks = reinterpret_cast<const uint32_t *>(kc + Sh::kCodes);
-      const uint8_t *vc = kc + Sh::kCodes + Sh::kState;
-      const uint32_t *vs = reinterpret_cast<const uint32_t *>(vc + Sh::kCodes);
-      const int key0 = (v.u0 + first + k) * kKvUnit;
+      const int key0 = (sg.v.u0 + sg.first + k) * kKvUnit;
       const uint32_t parts = (there >> (2 * st)) & 3u;
-      const bool inside = key0 >= lo_all && key0 + kKvUnit <= hi_all && (parts == 3u || (parts == 1u && part_log2 == 5));
-      // a key can be read: inside the lengths and its page was there
-      auto real_key = [&](int kk) {
-        return key0 + kk < hi_any && key0 + kk >= lo_any && ((parts >> (kk >> part_log2)) & 1u);
-      };
-      float sv[2][2][NB], zv[2][2][NB];  // [16-key tile][row g, g + 8][block]
-      float xs[2][NT][4], m_new[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) m_new[n][0] = m_new[n][1] = -INFINITY;
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        float acc[NT][NB][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < NB; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.0f;
-        uint32_t wa[W4], wb[W4];
-        const uint8_t *ra = kc + (16 * mt + g) * (D / 2) + t * (W4 * 4);
-        if constexpr (W4 == 4) {
-          const uint4 a = *reinterpret_cast<const uint4 *>(ra), bb = *reinterpret_cast<const uint4 *>(ra + 8 * (D / 2));
-          wa[0] = a.x, wa[1] = a.y, wa[2] = a.z, wa[3] = a.w;
-          wb[0] = bb.x, wb[1] = bb.y, wb[2] = bb.z, wb[3] = bb.w;
-        } else {
-          const uint2 a = *reinterpret_cast<const uint2 *>(ra), bb = *reinterpret_cast<const uint2 *>(ra + 8 * (D / 2));
-          wa[0] = a.x, wa[1] = a.y;
-          wb[0] = bb.x, wb[1] = bb.y;
-        }
-#pragma unroll
-        for (int w = 0; w < W4; ++w) {
-          const int j = w % NB;
-          const uint32_t a8 = wa[w] >> 8, b8 = wb[w] >> 8;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            uint32_t q0, q1, q2, q3;
-            if constexpr (NT == 1) {
-              q0 = qf[w][0], q1 = qf[w][1], q2 = qf[w][2], q3 = qf[w][3];
-            } else {
-              const uint4 q4v = *reinterpret_cast<const uint4 *>(s_q + (8 * n + g) * Sh::kQRow + (W4 * t + w) * 16);
-              q0 = q4v.x, q1 = q4v.y, q2 = q4v.z, q3 = q4v.w;
-            }
-            mma_f16(acc[n][j], wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u, wb[w] & 0x00F000F0u, q0, q1);
-            mma_f16(acc[n][j], a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, q2, q3);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int kk = 16 * mt + g + 8 * h;
-          const bool ok = inside || real_key(kk);
-          float sk[NB], sz[NB], top = 0.0f;
-#pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            const uint32_t a = ok ? ks[kk * NB + j] : 0u, c2 = ok ? vs[kk * NB + j] : 0u;
-            sk[j] = half_lo(a);
-            sz[j] = sk[j] * half_hi(a);
-            sv[mt][h][j] = half_lo(c2);
-            zv[mt][h][j] = half_hi(c2);
-            top = fmaxf(top, sv[mt][h][j]);
-          }
-          const float ev = (float)max((int)(__float_as_uint(top) >> 23) - 127, -24);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float s = 0.0f;
-#pragma unroll
-              for (int j = 0; j < NB; ++j) s += sk[j] * (acc[n][j][2 * h + e] * hf[n][e]) - sz[j] * qs[n][j][e];
-              if (!inside && (!ok || key0 + kk >= hi[n][e] || key0 + kk < lo[n][e])) s = -INFINITY;
-              xs[mt][n][2 * h + e] = s;
-              m_new[n][e] = fmaxf(m_new[n][e], s + ev);
-            }
-        }
-      }
-      bool grow = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) m_new[n][e] = fmaxf(m_new[n][e], __shfl_xor_sync(0xffffffffu, m_new[n][e], o));
-          grow |= m_new[n][e] > m_run[n][e] + kKvSlack;
-        }
-      if (__any_sync(0xffffffffu, grow)) {
-        // the maximum moves only when it grows by more than kKvSlack: the
-        // weights stay below 2^(kKvSlack + 1)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float to = fmaxf(m_run[n][e], m_new[n][e]);
-            const float f = m_run[n][e] == -INFINITY ? 0.0f : ex2(m_run[n][e] - to);
-            m_run[n][e] = to;
-            l_run[n][e] *= f;
-#pragma unroll
-            for (int j = 0; j < NB; ++j) zs[n][j][e] *= f;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) o_acc[n][m][e] *= f, o_acc[n][m][2 + e] *= f;
-          }
-      }
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        uint32_t bw[NT][NB][2];  // the weights as B operand: key pairs of one query row
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float pr[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float m = m_run[n][i & 1];
-            pr[i] = ex2(xs[mt][n][i] - (m == -INFINITY ? 0.0f : m));
-            l_run[n][i & 1] += pr[i];
-          }
-#pragma unroll
-          for (int j = 0; j < NB; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              // a masked weight is zero whatever the key's state holds
-              float w0 = pr[2 * h] * sv[mt][h][j], w1 = pr[2 * h + 1] * sv[mt][h][j];
-              if (!inside) {
-                if (xs[mt][n][2 * h] == -INFINITY) w0 = 0.0f;
-                if (xs[mt][n][2 * h + 1] == -INFINITY) w1 = 0.0f;
-              }
-              const uint32_t ww = Dt<Q4_F16>::pack2(w0, w1);
-              // the zero-points' part, with the weights as the MMAs see them
-              zs[n][j][0] = fmaf(half_lo(ww), zv[mt][h][j], zs[n][j][0]);
-              zs[n][j][1] = fmaf(half_hi(ww), zv[mt][h][j], zs[n][j][1]);
-              bw[n][j][h] = movmatrix(ww);
-            }
-        }
-        // values: keys 2t, 2t + 1, 2t + 8, 2t + 9 of the tile, this lane's words of each
-        constexpr int WS = D / 64;
-        uint32_t vw[4][WS];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint8_t *r = vc + (16 * mt + 2 * t + (i & 1) + 8 * (i >> 1)) * (D / 2) + g * (WS * 4);
-          if constexpr (WS == 2) {
-            const uint2 u = *reinterpret_cast<const uint2 *>(r);
-            vw[i][0] = u.x, vw[i][1] = u.y;
-          } else {
-            vw[i][0] = *reinterpret_cast<const uint32_t *>(r);
-          }
-        }
-#pragma unroll
-        for (int ws = 0; ws < WS; ++ws) {
-          const int j = ws % NB;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {  // elements 0..3, 4..7 of the words
-            const uint32_t sel = half ? 0x7632u : 0x5410u;
-            const uint32_t a = __byte_perm(vw[0][ws], vw[1][ws], sel), c2 = __byte_perm(vw[2][ws], vw[3][ws], sel);
-            const uint32_t a8 = a >> 8, c8 = c2 >> 8;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_f16(o_acc[n][4 * ws + 2 * half], a & 0x000F000Fu, a & 0x00F000F0u, c2 & 0x000F000Fu, c2 & 0x00F000F0u,
-                      bw[n][j][0], bw[n][j][1]);
-              mma_f16(o_acc[n][4 * ws + 2 * half + 1], a8 & 0x000F000Fu, a8 & 0x00F000F0u, c8 & 0x000F000Fu,
-                      c8 & 0x00F000F0u, bw[n][j][0], bw[n][j][1]);
-            }
-          }
-        }
-      }
+      const uint8_t *kc = ring + st * Sh::kStage;
+      if (key0 >= sg.lo_all && key0 + kKvUnit <= sg.hi_all && parts == (part_log2 == 5 ? 1u : 3u))
+        kv_unit<D, B, NT, false>(run, kc, s_q, key0, lane, sg.hi_any, sg.lo_any, parts, part_log2);
+      else
+        kv_unit<D, B, NT, true>(run, kc, s_q, key0, lane, sg.hi_any, sg.lo_any, parts, part_log2);
       __syncwarp();  // the stage has been read
       const int next = k + Sh::kStages * kKvWarps;
-      if (next < count) issue(next, pg_next, seq_no + Sh::kStages);
+      if (next < sg.count) issue(next, pg_next, seq_no + Sh::kStages);
       pg_next = page_of(next + kKvWarps);
+    }
+
+    // the next segment's copies start while this one's results are joined
+    const KvSegment<R> done = sg;
+    x += sg.count;
+    const bool more = x < x1;
+    if (more) {
+      locate();
+      begin();
     }
 
     // ---- the warps join ----
@@ -506,13 +576,13 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
-          l_run[n][e] += __shfl_xor_sync(0xffffffffu, l_run[n][e], o);
+          run.l[n][e] += __shfl_xor_sync(0xffffffffu, run.l[n][e], o);
 #pragma unroll
-          for (int j = 0; j < NB; ++j) zs[n][j][e] += __shfl_xor_sync(0xffffffffu, zs[n][j][e], o);
+          for (int j = 0; j < NB; ++j) run.zs[n][j][e] += __shfl_xor_sync(0xffffffffu, run.zs[n][j][e], o);
         }
         if (g == 0) {
-          s_m[warp * R + 8 * n + 2 * t + e] = m_run[n][e];
-          s_l[warp * R + 8 * n + 2 * t + e] = l_run[n][e];
+          s_m[warp * R + 8 * n + 2 * t + e] = run.m[n][e];
+          s_l[warp * R + 8 * n + 2 * t + e] = run.l[n][e];
         }
       }
     __syncthreads();
@@ -531,7 +601,7 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
           for (int e = 0; e < 2; ++e) {
             const int r = 8 * n + 2 * t + e;
             const float m = join_max(r);
-            const float f = m_run[n][e] == -INFINITY ? 0.0f : ex2(m_run[n][e] - m);
+            const float f = run.m[n][e] == -INFINITY ? 0.0f : ex2(run.m[n][e] - m);
 #pragma unroll
             for (int ws = 0; ws < D / 64; ++ws) {
               const int j = ws % NB;
@@ -540,8 +610,8 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 float2 val;
-                val.x = f * fmaf(o_acc[n][4 * ws + q][e], 16777216.0f, -zs[n][j][e]);
-                val.y = f * fmaf(o_acc[n][4 * ws + q][2 + e], 1048576.0f, -zs[n][j][e]);
+                val.x = f * fmaf(run.o[n][4 * ws + q][e], 16777216.0f, -run.zs[n][j][e]);
+                val.y = f * fmaf(run.o[n][4 * ws + q][2 + e], 1048576.0f, -run.zs[n][j][e]);
                 float2 *dst = reinterpret_cast<float2 *>(o + r * Sh::kORow + d0 + 2 * q);
                 if (add) {
                   const float2 old = *dst;
@@ -557,15 +627,16 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
       if (warp < 4) put(true);
       __syncthreads();
     }
-    const bool whole = count == v.units;
-    const int64_t seg0 = base + (int64_t)seg * v.units;  // the segment's units in the list
+    const int units = done.v.units, rows = done.rows;
+    const bool whole = done.count == units;
+    const int64_t seg0 = done.base + (int64_t)done.seg * units;  // the segment's units in the list
     auto owner = [&](int64_t u) { return (int)(((u + 1) * ctas - 1) / total); };
     auto part_of = [&](int cta) { return p.parts + ((int64_t)cta * 2 + (total * cta / ctas < seg0 ? 1 : 0)) * Sh::kPart; };
     // row r of the tile, elements d .. d + 3, from the sums o, the maximum and l
     auto finish = [&](int r, int d, float4 o, float m, float l) {
       if (r >= rows) return;
-      const int i = (r0 + r) / group, h = hk * group + (r0 + r) % group;
-      const int64_t at = (int64_t)(v.s.q0 + i) * p.q_heads + h;
+      const int i = (done.r0 + r) / group, h = done.hk * group + (done.r0 + r) % group;
+      const int64_t at = (int64_t)(done.v.s.q0 + i) * p.q_heads + h;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       uint2 out;
       out.x = Dt<DT>::pack2(o.x * inv, o.y * inv);
@@ -598,7 +669,7 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
     }
     if (!whole) {
       // the CTAs of the segment join: counted on the first one's word
-      const int c0 = owner(seg0), c1 = owner(seg0 + v.units - 1);
+      const int c0 = owner(seg0), c1 = owner(seg0 + units - 1);
       __threadfence();
       __syncthreads();
       if (tid == 0) {
@@ -611,6 +682,7 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
         __threadfence();
         for (int i = tid; i < R * D / 4; i += kKvAttnThreads) {
           const int r = i / (D / 4), d = i % (D / 4) * 4;
+          if (r >= rows) continue;
           float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           float m = -INFINITY, l = 0.0f;
           constexpr int kAhead = 8;  // partial results on their way at once
@@ -643,8 +715,8 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
         }
       }
     }
+    if (!more) break;
     __syncthreads();  // shared memory is free for the next segment
-    x += count;
   }
   if (s_abort) {
     // after a timeout the copies that nobody waits for get a millisecond
