@@ -75,6 +75,7 @@ __device__ __forceinline__ int kv_page(const KvAttnParams &p, int b, int i, int6
 
 constexpr int kKvUnit = 32;    // keys per unit
 constexpr int kKvWarps = 8;
+constexpr int kKvSegmentCost = 8;  // of a segment in units of the list, beside its units
 constexpr float kKvSlack = 8.0f;
 constexpr float kKvMasked = -3.4028235e38f;  // in the place of a score that does not count
 constexpr int kKvAttnThreads = kKvWarps * 32;
@@ -111,6 +112,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 // Transposes an 8 x 8 matrix of 16-bit values held two to a lane.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
   uint32_t r;
@@ -127,8 +135,7 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float half_lo(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu))); }
-__device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w >> 16))); }
+__device__ __forceinline__ float2 half_pair(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
 __device__ __forceinline__ void kv_bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
@@ -141,6 +148,7 @@ __device__ __forceinline__ void kv_bulk_load(uint32_t dst, const void *src, uint
 struct KvSpan {
   KvSeq s;
   int u0, units, rt;
+  int cost;  // units in the list: those, and kKvSegmentCost for a segment's begin and join
 };
 template <int R> __device__ __forceinline__ KvSpan kv_span(const KvAttnParams &p, int b, int group) {
   KvSpan v;
@@ -149,6 +157,7 @@ template <int R> __device__ __forceinline__ KvSpan kv_span(const KvAttnParams &p
   const int lo = p.window ? max(0, v.s.len - v.s.n - p.window + 1) : 0;
   v.u0 = lo / kKvUnit;
   v.units = v.s.n > 0 ? max(1, (v.s.len + kKvUnit - 1) / kKvUnit - v.u0) : 0;
+  v.cost = v.s.n > 0 ? v.units + kKvSegmentCost : 0;
   return v;
 }
 
@@ -169,12 +178,6 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt) {
     float acc[NT][NB][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.0f;
     uint32_t wa[W4], wb[W4];
     const uint8_t *ra = kc + (16 * mt + g) * (D / 2) + t * (W4 * 4);
     if constexpr (W4 == 4) {
@@ -193,7 +196,8 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint4 q = *reinterpret_cast<const uint4 *>(s_q + (8 * n + g) * Sh::kQRow + (W4 * t + w) * 16);
-        mma_f16(acc[n][j], wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u, wb[w] & 0x00F000F0u, q.x, q.y);
+        if (w < NB) mma_f16_first(acc[n][j], wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u, wb[w] & 0x00F000F0u, q.x, q.y);
+        else mma_f16(acc[n][j], wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u, wb[w] & 0x00F000F0u, q.x, q.y);
         mma_f16(acc[n][j], a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, q.z, q.w);
       }
     }
@@ -213,11 +217,10 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         if (!ok) ka[j] = va[j] = 0u;
-        sk[j] = half_lo(ka[j]);
-        sz[j] = sk[j] * half_hi(ka[j]);
-        sv[mt][h][j] = half_lo(va[j]);
-        zv[mt][h][j] = half_hi(va[j]);
-        top = fmaxf(top, sv[mt][h][j]);
+        const float2 k2 = half_pair(ka[j]), v2 = half_pair(va[j]);
+        sk[j] = k2.x, sz[j] = k2.x * k2.y;
+        sv[mt][h][j] = v2.x, zv[mt][h][j] = v2.y;
+        top = fmaxf(top, v2.x);
       }
       const float ev = fmaxf(lg2(top), -24.0f);
 #pragma unroll
@@ -290,8 +293,9 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
           }
           const uint32_t ww = Dt<Q4_F16>::pack2(w0, w1);
           // the zero-points' part, with the weights as the MMAs see them
-          run.zs[n][j][0] = fmaf(half_lo(ww), zv[mt][h][j], run.zs[n][j][0]);
-          run.zs[n][j][1] = fmaf(half_hi(ww), zv[mt][h][j], run.zs[n][j][1]);
+          const float2 wr = half_pair(ww);
+          run.zs[n][j][0] = fmaf(wr.x, zv[mt][h][j], run.zs[n][j][0]);
+          run.zs[n][j][1] = fmaf(wr.y, zv[mt][h][j], run.zs[n][j][1]);
           bw[n][j][h] = movmatrix(ww);
         }
       }
@@ -335,6 +339,7 @@ template <int R> struct KvSegment {
   int64_t base;            // the sequence's first unit in the list
   int b, seg, first, count;
   int r0, hk, rows;
+  int key0, key_end;                   // keys of the run (key_end: also where no row attends further)
   int hi_all, hi_any, lo_all, lo_any;  // keys that all and that some rows of the tile attend to
   __device__ __forceinline__ void ranges(const KvAttnParams &p, int group) {
     r0 = seg / p.c.heads * R, hk = seg % p.c.heads;
@@ -382,7 +387,7 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   int segs = 0;
   for (int b = tid * per; b < min(p.batch, (tid + 1) * per); ++b) {
     const KvSpan v = kv_span<R>(p, b, group);
-    mine += (int64_t)v.rt * p.c.heads * v.units;
+    mine += (int64_t)v.rt * p.c.heads * v.cost;
     segs += min(v.rt, 1 << 16) * p.c.heads;
   }
   int64_t incl = mine;
@@ -411,8 +416,11 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   if (segs <= (int)gridDim.x) ctas = segs * (int)min((int64_t)(gridDim.x / segs), (total + kKvWarps * segs - 1) / (kKvWarps * segs));
   const int c = blockIdx.x;
   if (c >= ctas) return;
-  int64_t x = total * c / ctas;
-  const int64_t x1 = total * (c + 1) / ctas;
+  const int64_t run = total / ctas;
+  const int longer = (int)(total - run * ctas);  // runs of one unit more
+  auto begin_of = [&](int cta) { return run * cta + min(cta, longer); };
+  int64_t x = begin_of(c);
+  const int64_t x1 = begin_of(c + 1);
   if (x >= incl - mine && x < incl) s_first[0] = tid * per, s_first[1] = incl - mine;
   __syncthreads();
   const int64_t pages = p.c.slots >> p.c.page_log2;
@@ -424,39 +432,52 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   sg.b = (int)s_first[0];
   sg.base = s_first[1];
   sg.v = kv_span<R>(p, sg.b, group);
-  auto locate = [&] {  // sg: the segment of unit x, as far as this CTA takes it
-    while (x >= sg.base + (int64_t)sg.v.rt * p.c.heads * sg.v.units) {
-      sg.base += (int64_t)sg.v.rt * p.c.heads * sg.v.units;
-      sg.v = kv_span<R>(p, ++sg.b, group);
+  // sg: the segment that unit x of the list belongs to, as far as this CTA
+  // takes it, and x past it; false where the run has no more
+  auto locate = [&]() -> bool {
+    while (x < x1) {
+      while (x >= sg.base + (int64_t)sg.v.rt * p.c.heads * sg.v.cost) {
+        sg.base += (int64_t)sg.v.rt * p.c.heads * sg.v.cost;
+        sg.v = kv_span<R>(p, ++sg.b, group);
+      }
+      sg.seg = (int)((x - sg.base) / sg.v.cost);
+      sg.first = (int)((x - sg.base) - (int64_t)sg.seg * sg.v.cost);
+      sg.count = (int)min((int64_t)(sg.v.units - sg.first), x1 - x);
+      x = min(x1, sg.base + (int64_t)(sg.seg + 1) * sg.v.cost);
+      if (sg.count > 0) break;  // else the run began in the segment's own cost
+      if (x >= x1) return false;
     }
-    sg.seg = (int)((x - sg.base) / sg.v.units);
-    sg.first = (int)((x - sg.base) - (int64_t)sg.seg * sg.v.units);
-    sg.count = (int)min((int64_t)(sg.v.units - sg.first), x1 - x);
     sg.ranges(p, group);
+    sg.key0 = (sg.v.u0 + sg.first) * kKvUnit;
+    sg.key_end = min(sg.hi_any, sg.key0 + sg.count * kKvUnit);
+    return true;
   };
-  // copies of unit first + k: lane 4 part + kind copies (codes or states of K
-  // or V) a page's part
-  auto page_of = [&](int k) -> int {  // page of this lane's part, -1 to leave it out
-    const int part = lane >> 2;
-    const int key = (sg.v.u0 + sg.first + k) * kKvUnit + (part << part_log2);
+  // copies of a unit: lane 4 part + kind copies (codes or states of K or V) a
+  // page's part; what does not change is kept per lane
+  const int part = lane >> 2, which = lane & 1;
+  const bool copier = part < (32 >> part_log2);
+  const uint32_t vec_bytes = (lane & 2) ? NB * 4 : D / 2;
+  const uint32_t copy_bytes = vec_bytes << part_log2;
+  const uint32_t copy_dst = ring_u + which * (Sh::kCodes + Sh::kState) + ((lane & 2) ? Sh::kCodes : 0) + part * copy_bytes;
+  const uint8_t *const copy_src = (lane & 2) ? reinterpret_cast<const uint8_t *>(p.c.state[which]) : p.c.codes[which];
+  const int key_off = part << part_log2;
+  auto page_of = [&](int key) -> int {  // page of this lane's part of the unit at `key`, -1 to leave it out
+    key += key_off;
     // parts outside what any row attends to may have no page: left out
-    if (k >= sg.count || part >= (32 >> part_log2) || key >= sg.hi_any || key + (1 << part_log2) <= sg.lo_any) return -1;
+    if (!copier || key >= sg.key_end || key + (1 << part_log2) <= sg.lo_any) return -1;
     return kv_page(p, sg.b, key >> p.c.page_log2, pages);
   };
   uint32_t there = 0;  // bit stage * 2 + part: the part was copied
-  auto issue = [&](int k, int pg, uint32_t no) {
-    const int st = no % Sh::kStages, part = lane >> 2, kind = lane & 3, which = kind & 1;
+  auto issue = [&](int key, int pg, uint32_t no) {
+    const int st = no % Sh::kStages;
     const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0);
-    there = (there & ~(3u << (2 * st))) | (((ok & 1u) | ((ok >> 3) & 2u)) << (2 * st));
-    const uint32_t parts = __popc(ok & 0x11u), keys = 1u << part_log2;
-    if (lane == 0) mbar_arrive_expect_tx(bar + 8 * st, parts * 2 * keys * (D / 2 + NB * 4));
+    const uint32_t parts = (ok & 1u) | ((ok >> 3) & 2u);
+    there = (there & ~(3u << (2 * st))) | (parts << (2 * st));
+    if (lane == 0) mbar_arrive_expect_tx(bar + 8 * st, (__popc(parts) * 2 * (D / 2 + NB * 4)) << part_log2);
     __syncwarp();
     if (pg >= 0) {
-      const int key = (sg.v.u0 + sg.first + k) * kKvUnit + (part << part_log2);
-      const int64_t vec = ((((int64_t)pg * p.c.heads + sg.hk) << p.c.page_log2) + (key & page_mask));
-      const uint32_t dst = ring_u + st * Sh::kStage + which * (Sh::kCodes + Sh::kState);
-      if (kind < 2) kv_bulk_load(dst + part * keys * (D / 2), p.c.codes[which] + vec * (D / 2), keys * (D / 2), bar + 8 * st);
-      else kv_bulk_load(dst + Sh::kCodes + part * keys * NB * 4, p.c.state[which] + vec * NB, keys * NB * 4, bar + 8 * st);
+      const uint64_t vec = ((uint64_t)(uint32_t)(pg * p.c.heads + sg.hk) << p.c.page_log2) + (uint32_t)((key + key_off) & page_mask);
+      kv_bulk_load(copy_dst + st * Sh::kStage, copy_src + vec * vec_bytes, copy_bytes, bar + 8 * st);
     }
   };
   uint32_t seq_no = 0;  // stages this warp has used
@@ -468,8 +489,8 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   auto begin = [&] {
     int pg[Sh::kStages];
 #pragma unroll
-    for (int s = 0; s < Sh::kStages; ++s) pg[s] = page_of(warp + s * kKvWarps);
-    pg_next = page_of(warp + Sh::kStages * kKvWarps);
+    for (int s = 0; s < Sh::kStages; ++s) pg[s] = page_of(sg.key0 + (warp + s * kKvWarps) * kKvUnit);
+    pg_next = page_of(sg.key0 + (warp + Sh::kStages * kKvWarps) * kKvUnit);
 #pragma unroll
     for (int i = 0; i < Sh::kRowsPerWarp; ++i) {
       const int r = warp + i * kKvWarps, row = sg.r0 + r;
@@ -480,9 +501,9 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
     }
 #pragma unroll
     for (int s = 0; s < Sh::kStages; ++s)
-      if (warp + s * kKvWarps < sg.count) issue(warp + s * kKvWarps, pg[s], seq_no + s);
+      if (warp + s * kKvWarps < sg.count) issue(sg.key0 + (warp + s * kKvWarps) * kKvUnit, pg[s], seq_no + s);
   };
-  locate();
+  if (!locate()) return;
   begin();
 
   while (true) {
@@ -525,49 +546,44 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
     }
     __syncthreads();
 
-    KvRun<D, B, NT> run;
+    KvRun<D, B, NT> acc;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * n + 2 * t + e;
-        run.hf[n][e] = s_hf[r];
+        acc.hf[n][e] = s_hf[r];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) run.qs[n][j][e] = s_qs[j][r], run.zs[n][j][e] = 0.0f;
-        run.m[n][e] = -INFINITY, run.l[n][e] = 0.0f;
+        for (int j = 0; j < NB; ++j) acc.qs[n][j][e] = s_qs[j][r], acc.zs[n][j][e] = 0.0f;
+        acc.m[n][e] = -INFINITY, acc.l[n][e] = 0.0f;
         const int i = (sg.r0 + r) / group;
-        run.hi[n][e] = sg.hi(p, i), run.lo[n][e] = sg.lo(p, i);
+        acc.hi[n][e] = sg.hi(p, i), acc.lo[n][e] = sg.lo(p, i);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) run.o[n][m][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) acc.o[n][m][e] = 0.0f;
     }
 
-    for (int k = warp; k < sg.count; k += kKvWarps, ++seq_no) {
+    int key = sg.key0 + warp * kKvUnit;
+    for (int k = warp; k < sg.count; k += kKvWarps, ++seq_no, key += kKvWarps * kKvUnit) {
       const int st = seq_no % Sh::kStages;
-      if (!mbar_wait_warp(bar + 8 * st, (seq_no / Sh::kStages) & 1, p.status, &s_abort, p.wait_ns)) break;
-      const int key0 = (sg.v.u0 + sg.first + k) * kKvUnit;
+      if (!mbar_wait(bar + 8 * st, (seq_no / Sh::kStages) & 1, p.status, &s_abort, p.wait_ns)) break;
       const uint32_t parts = (there >> (2 * st)) & 3u;
       const uint8_t *kc = ring + st * Sh::kStage;
-      if (key0 >= sg.lo_all && key0 + kKvUnit <= sg.hi_all && parts == (part_log2 == 5 ? 1u : 3u))
-        kv_unit<D, B, NT, false>(run, kc, s_q, key0, lane, sg.hi_any, sg.lo_any, parts, part_log2);
+      if (key >= sg.lo_all && key + kKvUnit <= sg.hi_all && parts == (part_log2 == 5 ? 1u : 3u))
+        kv_unit<D, B, NT, false>(acc, kc, s_q, key, lane, sg.hi_any, sg.lo_any, parts, part_log2);
       else
-        kv_unit<D, B, NT, true>(run, kc, s_q, key0, lane, sg.hi_any, sg.lo_any, parts, part_log2);
+        kv_unit<D, B, NT, true>(acc, kc, s_q, key, lane, sg.hi_any, sg.lo_any, parts, part_log2);
       __syncwarp();  // the stage has been read
-      const int next = k + Sh::kStages * kKvWarps;
-      if (next < sg.count) issue(next, pg_next, seq_no + Sh::kStages);
-      pg_next = page_of(next + kKvWarps);
+      if (k + Sh::kStages * kKvWarps < sg.count) issue(key + Sh::kStages * kKvWarps * kKvUnit, pg_next, seq_no + Sh::kStages);
+      pg_next = page_of(key + (Sh::kStages + 1) * kKvWarps * kKvUnit);
     }
 
     // the next segment's copies start while this one's results are joined
     const KvSegment<R> done = sg;
-    x += sg.count;
-    const bool more = x < x1;
-    if (more) {
-      locate();
-      begin();
-    }
+    const bool more = x < x1 && locate();
+    if (more) begin();
 
     // ---- the warps join ----
 #pragma unroll
@@ -576,13 +592,13 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
-          run.l[n][e] += __shfl_xor_sync(0xffffffffu, run.l[n][e], o);
+          acc.l[n][e] += __shfl_xor_sync(0xffffffffu, acc.l[n][e], o);
 #pragma unroll
-          for (int j = 0; j < NB; ++j) run.zs[n][j][e] += __shfl_xor_sync(0xffffffffu, run.zs[n][j][e], o);
+          for (int j = 0; j < NB; ++j) acc.zs[n][j][e] += __shfl_xor_sync(0xffffffffu, acc.zs[n][j][e], o);
         }
         if (g == 0) {
-          s_m[warp * R + 8 * n + 2 * t + e] = run.m[n][e];
-          s_l[warp * R + 8 * n + 2 * t + e] = run.l[n][e];
+          s_m[warp * R + 8 * n + 2 * t + e] = acc.m[n][e];
+          s_l[warp * R + 8 * n + 2 * t + e] = acc.l[n][e];
         }
       }
     __syncthreads();
@@ -601,7 +617,7 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
           for (int e = 0; e < 2; ++e) {
             const int r = 8 * n + 2 * t + e;
             const float m = join_max(r);
-            const float f = run.m[n][e] == -INFINITY ? 0.0f : ex2(run.m[n][e] - m);
+            const float f = acc.m[n][e] == -INFINITY ? 0.0f : ex2(acc.m[n][e] - m);
 #pragma unroll
             for (int ws = 0; ws < D / 64; ++ws) {
               const int j = ws % NB;
@@ -610,8 +626,8 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 float2 val;
-                val.x = f * fmaf(run.o[n][4 * ws + q][e], 16777216.0f, -run.zs[n][j][e]);
-                val.y = f * fmaf(run.o[n][4 * ws + q][2 + e], 1048576.0f, -run.zs[n][j][e]);
+                val.x = f * fmaf(acc.o[n][4 * ws + q][e], 16777216.0f, -acc.zs[n][j][e]);
+                val.y = f * fmaf(acc.o[n][4 * ws + q][2 + e], 1048576.0f, -acc.zs[n][j][e]);
                 float2 *dst = reinterpret_cast<float2 *>(o + r * Sh::kORow + d0 + 2 * q);
                 if (add) {
                   const float2 old = *dst;
@@ -629,9 +645,8 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
     }
     const int units = done.v.units, rows = done.rows;
     const bool whole = done.count == units;
-    const int64_t seg0 = done.base + (int64_t)done.seg * units;  // the segment's units in the list
-    auto owner = [&](int64_t u) { return (int)(((u + 1) * ctas - 1) / total); };
-    auto part_of = [&](int cta) { return p.parts + ((int64_t)cta * 2 + (total * cta / ctas < seg0 ? 1 : 0)) * Sh::kPart; };
+    const int64_t seg0 = done.base + (int64_t)done.seg * done.v.cost;  // the segment's units in the list
+    auto part_of = [&](int cta) { return p.parts + ((int64_t)cta * 2 + (begin_of(cta) < seg0 ? 1 : 0)) * Sh::kPart; };
     // row r of the tile, elements d .. d + 3, from the sums o, the maximum and l
     auto finish = [&](int r, int d, float4 o, float m, float l) {
       if (r >= rows) return;
@@ -669,7 +684,9 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
     }
     if (!whole) {
       // the CTAs of the segment join: counted on the first one's word
-      const int c0 = owner(seg0), c1 = owner(seg0 + units - 1);
+      int c0 = c, c1 = c;
+      while (begin_of(c0) > seg0) --c0;
+      while (begin_of(c1 + 1) < seg0 + units) ++c1;
       __threadfence();
       __syncthreads();
       if (tid == 0) {
