@@ -13,10 +13,14 @@
 //  - mma.sync m16n8k16, keys on the 16-row side, query rows (8 or 16 of the
 //    rows that share a kv head) on the 8-column side.  The contraction over d
 //    may run in any order, so a lane takes the words of a row as they lie.
-//  - Online softmax in base 2 with the running maximum of score +
-//    exponent(s_v): the weights w <= 2^9 then use binary16's range well
-//    whatever the values' sizes.  Query rows are scaled by a power of two into
-//    binary16 (exact for both 16-bit types down to 2^-38 of the row's largest).
+//  - Online softmax in base 2 with a running reference m near the maximum of
+//    score + log2(s_v), so that the weights w = 2^(score - m) s_v use binary16's
+//    range well whatever the values' sizes.  m moves only when a weight leaves
+//    that range (a packed maximum finds it), which is rare after the first
+//    unit: no reduction over lanes and no rescaling in the common case.  The
+//    zero-points' sum is one more MMA with the weights.  Query rows are scaled
+//    by a power of two into binary16 (exact for both 16-bit types down to 2^-38
+//    of the row's largest).
 // Work: the (sequence, row tile, kv head) segments, each in units of 32 keys,
 // are one list that is cut into equal runs, one per CTA, whatever the lengths;
 // a CTA's 8 warps take its units in turn, each with its own ring of bulk
@@ -25,6 +29,8 @@
 // tile below 128 rows on the key side that would pay for 8 query rows, and
 // needs dequantized operands in shared memory; here registers feed the MMAs.)
 #pragma once
+#include <limits.h>
+
 #include "gemm.cuh"  // PTX wrappers, bounded waits
 #include "kv_cache.cuh"
 
@@ -64,19 +70,10 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnParams &p, int b) {
   if (s.q0 != q0 || s.q0 + s.n != q1 || s.len != len) raise_status(p.status, Q4_STATUS_INDEX);
   return s;
 }
-// Page of key block `i` of sequence b, or -1 with the status raised.
-__device__ __forceinline__ int kv_page(const KvAttnParams &p, int b, int i, int64_t pages) {
-  const int pg = __ldg(p.table + (int64_t)b * p.table_stride + i);
-  if (pg >= 0 && pg < pages) return pg;
-  raise_status(p.status, Q4_STATUS_INDEX);
-  return -1;
-}
-
 
 constexpr int kKvUnit = 32;    // keys per unit
 constexpr int kKvWarps = 8;
 constexpr int kKvSegmentCost = 8;  // of a segment in units of the list, beside its units
-constexpr float kKvSlack = 8.0f;
 constexpr float kKvMasked = -3.4028235e38f;  // in the place of a score that does not count
 constexpr int kKvAttnThreads = kKvWarps * 32;
 constexpr size_t kKvCountBytes = Q4_WORKSPACE_HEAD;
@@ -89,40 +86,29 @@ template <int D, int B, int NT> struct KvShape {
   static constexpr int kStages = NT == 1 ? 2 : 4;
   static constexpr int kQRow = D * 2 + 16;   // bytes of a query row in shared memory
   static constexpr int kORow = D + 4;        // floats of an output row
+  static constexpr int kFactors = 4 * kORow > 320 ? 4 * kORow : 320;  // most CTAs of a segment
   static constexpr int kRing = kKvWarps * kStages * kStage;
-  static constexpr int kSmem = kRing + R * kQRow + 4 * R * kORow * 4 + 2 * kKvWarps * R * 4;
+  static constexpr int kSmem = kRing + R * kQRow + R * kFactors * 4 + 2 * kKvWarps * R * 4;
   static constexpr int kPart = R * (D + 2);  // floats of a partial result: O, then M and l
   static constexpr int kRowsPerWarp = (R + kKvWarps - 1) / kKvWarps;
 };
 
-// What a warp keeps of its query rows over a segment: columns 8 n + 2 t + e.
-template <int D, int B, int NT> struct KvRun {
-  static constexpr int NB = D / B;
-  float o[NT][D / 16][4];           // output^T: rows d, columns query rows
-  float m[NT][2], l[NT][2];         // running maximum, sum of weights over exponents
-  float zs[NT][NB][2];              // sum w z per block
-  float hf[NT][2], qs[NT][NB][2];   // score factor, the query's block sums
-  int hi[NT][2], lo[NT][2];         // keys the row attends to
-};
-
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // Transposes an 8 x 8 matrix of 16-bit values held two to a lane.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -136,11 +122,26 @@ __device__ __forceinline__ float lg2(float x) {
   return r;
 }
 __device__ __forceinline__ float2 half_pair(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+// Issued where it stands: a batch of them is on its way at once.
+__device__ __forceinline__ float4 ldcg_v4(const float *p) {
+  float4 r;
+  asm volatile("ld.global.cg.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "l"(p) : "memory");
+  return r;
+}
 __device__ __forceinline__ void kv_bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
       "r"(bytes), "r"(bar)
       : "memory");
+}
+
+// a / b for a >= 0, b > 0: in 32 bits where they are enough.
+__device__ __forceinline__ int64_t kv_div(int64_t a, int b) {
+  return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+__device__ __forceinline__ int64_t kv_div64(int64_t a, int64_t b) {
+  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
 // The units of sequence b: u0 .. u0 + units - 1 (at least one where it has
@@ -161,20 +162,33 @@ template <int R> __device__ __forceinline__ KvSpan kv_span(const KvAttnParams &p
   return v;
 }
 
-// One unit: 32 keys whose codes and states lie in shared memory.  MASK: some
-// key is outside some row's range, or its page was not there.
-template <int D, int B, int NT, bool MASK>
-__device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc, const uint8_t *s_q, int key0, int lane,
-                                        int hi_any, int lo_any, uint32_t parts, int part_log2) {
+// What a warp keeps of its query rows over a segment: columns 8 n + 2 t + e.
+template <int D, int B, int NT> struct KvRun {
+  static constexpr int NB = D / B;
+  float o[NT][D / 16][4];           // output^T: rows d, columns query rows
+  float zs[NT][NB][4];              // sum w z per block (all rows alike)
+  float m[NT][2], l[NT][2];         // reference (-inf before the first key), sum of 2^(score - m)
+  float hf[NT][2], qs[NT][NB][2];   // score factor, the query's block sums
+  bool pending;                     // a row has no reference yet
+};
+
+// One unit: 32 keys whose codes and states lie in shared memory.  inside: all
+// of them count for every row; else hi, lo (in shared memory) bound a row's
+// keys, and hi_any, lo_any and parts say which keys can be read at all.
+template <int D, int B, int NT, bool inside>
+__device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc, const uint8_t *s_q, const int *s_hi,
+                                        const int *s_lo, int key0, int lane, bool first, int hi_any, int lo_any,
+                                        uint32_t parts, int part_log2) {
   using Sh = KvShape<D, B, NT>;
   constexpr int NB = Sh::NB, W4 = D / 32, MT = D / 16;
   const int g = lane >> 2, t = lane & 3;
   const uint8_t *ks = kc + Sh::kCodes, *vc = ks + Sh::kState, *vs = vc + Sh::kCodes;
-  float sv[2][2][NB], zv[2][2][NB];  // [16-key tile][row g, g + 8][block]
-  float xs[2][NT][4];                // scores before the factor hf
-  float m_new[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) m_new[n][0] = m_new[n][1] = -INFINITY;
+  // a key can be read: inside the lengths, and its page was there
+  auto real_key = [&](int kk) {
+    return key0 + kk < hi_any && key0 + kk >= lo_any && ((parts >> (kk >> part_log2)) & 1u);
+  };
+  float sv[2][2][NB];   // values' scales, [16-key tile][row g, g + 8][block]
+  float xs[2][NT][4];   // scores before the factor hf
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt) {
     float acc[NT][NB][4];
@@ -204,8 +218,7 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int kk = 16 * mt + g + 8 * h;
-      // a key can be read: inside the lengths, and its page was there
-      const bool ok = !MASK || (key0 + kk < hi_any && key0 + kk >= lo_any && ((parts >> (kk >> part_log2)) & 1u));
+      float sk[NB], sz[NB];
       uint32_t ka[NB], va[NB];
       if constexpr (NB == 2) {
         const uint2 u = *reinterpret_cast<const uint2 *>(ks + kk * 8), w = *reinterpret_cast<const uint2 *>(vs + kk * 8);
@@ -213,16 +226,12 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
       } else {
         ka[0] = *reinterpret_cast<const uint32_t *>(ks + kk * 4), va[0] = *reinterpret_cast<const uint32_t *>(vs + kk * 4);
       }
-      float sk[NB], sz[NB], top = 0.0f;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        if (!ok) ka[j] = va[j] = 0u;
-        const float2 k2 = half_pair(ka[j]), v2 = half_pair(va[j]);
+        const float2 k2 = half_pair(ka[j]);
         sk[j] = k2.x, sz[j] = k2.x * k2.y;
-        sv[mt][h][j] = v2.x, zv[mt][h][j] = v2.y;
-        top = fmaxf(top, v2.x);
+        sv[mt][h][j] = half_pair(va[j]).x;
       }
-      const float ev = fmaxf(lg2(top), -24.0f);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -231,30 +240,46 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
           if constexpr (NB == 2) s = fmaf(sk[1], acc[n][1][2 * h + e], s);
 #pragma unroll
           for (int j = 0; j < NB; ++j) s = fmaf(-sz[j], run.qs[n][j][e], s);
-          float x = fmaf(s, run.hf[n][e], ev);
-          if (MASK && (!ok || key0 + kk >= run.hi[n][e] || key0 + kk < run.lo[n][e])) x = -INFINITY, s = kKvMasked;
           xs[mt][n][2 * h + e] = s;
-          m_new[n][e] = fmaxf(m_new[n][e], x);
         }
     }
-  }
-  bool grow = false;
+    if (!inside) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+      for (int h = 0; h < 2; ++h) {
+        const int kk = 16 * mt + g + 8 * h;
+        const bool ok = real_key(kk);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+        for (int j = 0; j < NB; ++j)
+          if (!ok) sv[mt][h][j] = 0.0f;
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) m_new[n][e] = fmaxf(m_new[n][e], __shfl_xor_sync(0xffffffffu, m_new[n][e], o));
-      grow |= m_new[n][e] > run.m[n][e] + kKvSlack;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * n + 2 * t + e;
+            if (!ok || key0 + kk >= s_hi[r] || key0 + kk < s_lo[r]) xs[mt][n][2 * h + e] = kKvMasked;
+          }
+      }
     }
-  if (__any_sync(0xffffffffu, grow)) {
-    // the maximum moves only when it grows by more than kKvSlack: the weights
-    // stay below 2^(kKvSlack + 1)
+  }
+  // the reference moves to the maximum so far of score + log2(s_v)
+  auto move = [&] {
+    run.pending = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float to = fmaxf(run.m[n][e], m_new[n][e]);
+        float to = run.m[n][e];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float top = sv[mt][h][0];
+            if constexpr (NB == 2) top = fmaxf(top, sv[mt][h][1]);
+            const float s = xs[mt][n][2 * h + e];
+            if (s != kKvMasked) to = fmaxf(to, fmaf(s, run.hf[n][e], fmaxf(lg2(top), -24.0f)));
+          }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
         const float f = run.m[n][e] == -INFINITY ? 0.0f : ex2(run.m[n][e] - to);
         run.m[n][e] = to;
         run.l[n][e] *= f;
@@ -262,44 +287,92 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
         for (int j = 0; j < NB; ++j) run.zs[n][j][e] *= f;
 #pragma unroll
         for (int m = 0; m < MT; ++m) run.o[n][m][e] *= f, run.o[n][m][2 + e] *= f;
+        run.pending |= __any_sync(0xffffffffu, to == -INFINITY) != 0;
       }
+  };
+  uint32_t ww[2][NT][NB][2];  // weights, pairs of query rows
+  float lsum[NT][2];
+  auto weigh = [&]() -> uint32_t {  // the largest weight's bits, in either half
+    uint32_t top = 0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float mm[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) mm[e] = run.m[n][e] == -INFINITY ? 0.0f : -run.m[n][e], lsum[n][e] = 0.0f;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float pr[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) pr[e] = ex2(fmaf(xs[mt][n][2 * h + e], run.hf[n][e], mm[e]));
+          float w[NB][2];
+#pragma unroll
+          for (int j = 0; j < NB; ++j) w[j][0] = pr[0] * sv[mt][h][j], w[j][1] = pr[1] * sv[mt][h][j];
+          if (!inside) {  // a masked weight is zero whatever the key's state holds
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (xs[mt][n][2 * h + e] == kKvMasked) {
+                pr[e] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) w[j][e] = 0.0f;
+              }
+          }
+          lsum[n][0] += pr[0], lsum[n][1] += pr[1];
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            ww[mt][n][j][h] = Dt<Q4_F16>::pack2(w[j][0], w[j][1]);
+            top = __vmaxu2(top, ww[mt][n][j][h]);
+          }
+        }
+    }
+    return top;
+  };
+  if (first || !inside || run.pending) move();
+  const uint32_t top = weigh();
+  if (__any_sync(0xffffffffu, (top & 0xFFFFu) >= 0x7C00u || (top >> 16) >= 0x7C00u)) {  // past binary16
+    move();
+    weigh();
   }
-  float mm[NT][2];  // minus the maximum
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) mm[n][e] = run.m[n][e] == -INFINITY ? 0.0f : -run.m[n][e];
+  for (int n = 0; n < NT; ++n) run.l[n][0] += lsum[n][0], run.l[n][1] += lsum[n][1];
 #pragma unroll
   for (int mt = 0; mt < 2; ++mt) {
     uint32_t bw[NT][NB][2];  // the weights as B operand: key pairs of one query row
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float pr[2];
+      for (int j = 0; j < NB; ++j) bw[n][j][0] = movmatrix(ww[mt][n][j][0]), bw[n][j][1] = movmatrix(ww[mt][n][j][1]);
+    // zero-points of keys 2t, 2t + 1 and 2t + 8, 2t + 9, the same in all rows
+    uint32_t z[NB][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float s = xs[mt][n][2 * h + e];
-          pr[e] = ex2(fmaf(s, run.hf[n][e], mm[n][e]));
-          if (MASK && s == kKvMasked) pr[e] = 0.0f;
-          run.l[n][e] += pr[e];
-        }
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          float w0 = pr[0] * sv[mt][h][j], w1 = pr[1] * sv[mt][h][j];
-          if (MASK) {  // a masked weight is zero whatever the key's state holds
-            if (xs[mt][n][2 * h] == kKvMasked) w0 = 0.0f;
-            if (xs[mt][n][2 * h + 1] == kKvMasked) w1 = 0.0f;
-          }
-          const uint32_t ww = Dt<Q4_F16>::pack2(w0, w1);
-          // the zero-points' part, with the weights as the MMAs see them
-          const float2 wr = half_pair(ww);
-          run.zs[n][j][0] = fmaf(wr.x, zv[mt][h][j], run.zs[n][j][0]);
-          run.zs[n][j][1] = fmaf(wr.y, zv[mt][h][j], run.zs[n][j][1]);
-          bw[n][j][h] = movmatrix(ww);
-        }
+    for (int h = 0; h < 2; ++h) {
+      const int kk = 16 * mt + 2 * t + 8 * h;
+      uint32_t a[NB], c[NB];
+      if constexpr (NB == 2) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(vs + kk * 8);
+        a[0] = u.x, a[1] = u.y, c[0] = u.z, c[1] = u.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(vs + kk * 4);
+        a[0] = u.x, c[0] = u.y;
       }
-    // values: keys 2t, 2t + 1, 2t + 8, 2t + 9 of the tile, this lane's words of each
+#pragma unroll
+      for (int j = 0; j < NB; ++j) z[j][h] = __byte_perm(a[j], c[j], 0x7632u);
+    }
+    if (!inside) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int kk = 16 * mt + 2 * t + 8 * h;
+        const uint32_t keep = (real_key(kk) ? 0xFFFFu : 0u) | (real_key(kk + 1) ? 0xFFFF0000u : 0u);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) z[j][h] &= keep;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) mma_f16(run.zs[n][j], z[j][0], z[j][0], z[j][1], z[j][1], bw[n][j][0], bw[n][j][1]);
+    // values: the same keys, this lane's words of each
     constexpr int WS = D / 64;
     uint32_t vw[4][WS];
     const uint8_t *rv = vc + (16 * mt + 2 * t) * (D / 2) + g * (WS * 4);
@@ -363,10 +436,11 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   pdl_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *s_q = smem + Sh::kRing;
-  float *s_o = reinterpret_cast<float *>(s_q + R * Sh::kQRow);  // [4][R][kORow]
-  float *s_m = s_o + 4 * R * Sh::kORow, *s_l = s_m + kKvWarps * R;
+  float *s_o = reinterpret_cast<float *>(s_q + R * Sh::kQRow);  // [4][R][kORow], then [R][kFactors]
+  float *s_m = s_o + R * Sh::kFactors, *s_l = s_m + kKvWarps * R;
   __shared__ uint64_t s_bar[kKvWarps * Sh::kStages];
   __shared__ float s_hf[R], s_qs[NB][R];
+  __shared__ int s_hi[R], s_lo[R];
   __shared__ int64_t s_scan[kKvWarps], s_first[2];
   __shared__ int s_segs[kKvWarps], s_abort;
   __shared__ unsigned s_last;
@@ -381,12 +455,15 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   if (tid == 0) s_abort = 0;
   pdl_wait();
 
-  // this CTA's run of the list of units: a prefix sum over the sequences
+  // this CTA's run of the list of units: a prefix sum over the sequences (the
+  // spans of a batch of up to 256 stay in shared memory)
+  __shared__ KvSpan s_span[kKvAttnThreads];
   const int per = (p.batch + kKvAttnThreads - 1) / kKvAttnThreads;
   int64_t mine = 0;
   int segs = 0;
   for (int b = tid * per; b < min(p.batch, (tid + 1) * per); ++b) {
     const KvSpan v = kv_span<R>(p, b, group);
+    if (per == 1) s_span[b] = v;
     mine += (int64_t)v.rt * p.c.heads * v.cost;
     segs += min(v.rt, 1 << 16) * p.c.heads;
   }
@@ -412,18 +489,17 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   // all CTAs, or where that leaves less than a unit for each warp, fewer; a
   // multiple of the segments where there are few: equal ones are then cut
   // alike, and none lies in two pieces of one CTA
-  int ctas = (int)min((int64_t)gridDim.x, (total + kKvWarps - 1) / kKvWarps);
-  if (segs <= (int)gridDim.x) ctas = segs * (int)min((int64_t)(gridDim.x / segs), (total + kKvWarps * segs - 1) / (kKvWarps * segs));
+  const int grid = min((int)gridDim.x, Sh::kFactors);
+  int ctas = (int)min((int64_t)grid, (total + kKvWarps - 1) / kKvWarps);
+  if (segs <= grid) ctas = segs * (int)min((int64_t)(grid / segs), kv_div(total + kKvWarps * segs - 1, kKvWarps * segs));
   const int c = blockIdx.x;
   if (c >= ctas) return;
-  const int64_t run = total / ctas;
-  const int longer = (int)(total - run * ctas);  // runs of one unit more
-  auto begin_of = [&](int cta) { return run * cta + min(cta, longer); };
+  auto begin_of = [&](int cta) { return kv_div(total * cta, ctas); };
   int64_t x = begin_of(c);
   const int64_t x1 = begin_of(c + 1);
   if (x >= incl - mine && x < incl) s_first[0] = tid * per, s_first[1] = incl - mine;
   __syncthreads();
-  const int64_t pages = p.c.slots >> p.c.page_log2;
+  const int pages = (int)(p.c.slots >> p.c.page_log2);
   const int page_mask = (1 << p.c.page_log2) - 1;
   const int part_log2 = min(p.c.page_log2, 5);  // keys of a part: a page's, at most a unit's
   constexpr float kLog2e = 1.4426950408889634f;
@@ -431,16 +507,17 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   KvSegment<R> sg;
   sg.b = (int)s_first[0];
   sg.base = s_first[1];
-  sg.v = kv_span<R>(p, sg.b, group);
+  auto span_of = [&](int b) { return per == 1 ? s_span[b] : kv_span<R>(p, b, group); };
+  sg.v = span_of(sg.b);
   // sg: the segment that unit x of the list belongs to, as far as this CTA
   // takes it, and x past it; false where the run has no more
   auto locate = [&]() -> bool {
     while (x < x1) {
       while (x >= sg.base + (int64_t)sg.v.rt * p.c.heads * sg.v.cost) {
         sg.base += (int64_t)sg.v.rt * p.c.heads * sg.v.cost;
-        sg.v = kv_span<R>(p, ++sg.b, group);
+        sg.v = span_of(++sg.b);
       }
-      sg.seg = (int)((x - sg.base) / sg.v.cost);
+      sg.seg = (int)kv_div(x - sg.base, sg.v.cost);
       sg.first = (int)((x - sg.base) - (int64_t)sg.seg * sg.v.cost);
       sg.count = (int)min((int64_t)(sg.v.units - sg.first), x1 - x);
       x = min(x1, sg.base + (int64_t)(sg.seg + 1) * sg.v.cost);
@@ -461,32 +538,39 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   const uint32_t copy_dst = ring_u + which * (Sh::kCodes + Sh::kState) + ((lane & 2) ? Sh::kCodes : 0) + part * copy_bytes;
   const uint8_t *const copy_src = (lane & 2) ? reinterpret_cast<const uint8_t *>(p.c.state[which]) : p.c.codes[which];
   const int key_off = part << part_log2;
-  auto page_of = [&](int key) -> int {  // page of this lane's part of the unit at `key`, -1 to leave it out
+  const int32_t *table = nullptr;  // the segment's row of the table
+  constexpr int kNoPage = INT_MIN;
+  // the table's entry for this lane's part of the unit at `key` (looked at
+  // only when the copy is issued, a unit later)
+  auto page_of = [&](int key) -> int {
     key += key_off;
     // parts outside what any row attends to may have no page: left out
-    if (!copier || key >= sg.key_end || key + (1 << part_log2) <= sg.lo_any) return -1;
-    return kv_page(p, sg.b, key >> p.c.page_log2, pages);
+    if (!copier || key >= sg.key_end || key + (1 << part_log2) <= sg.lo_any) return kNoPage;
+    return __ldg(table + (key >> p.c.page_log2));
   };
   uint32_t there = 0;  // bit stage * 2 + part: the part was copied
   auto issue = [&](int key, int pg, uint32_t no) {
     const int st = no % Sh::kStages;
-    const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0);
+    const bool good = pg >= 0 && pg < pages;
+    if (!good && pg != kNoPage) raise_status(p.status, Q4_STATUS_INDEX);
+    const uint32_t ok = __ballot_sync(0xffffffffu, good);
     const uint32_t parts = (ok & 1u) | ((ok >> 3) & 2u);
     there = (there & ~(3u << (2 * st))) | (parts << (2 * st));
     if (lane == 0) mbar_arrive_expect_tx(bar + 8 * st, (__popc(parts) * 2 * (D / 2 + NB * 4)) << part_log2);
     __syncwarp();
-    if (pg >= 0) {
+    if (good) {
       const uint64_t vec = ((uint64_t)(uint32_t)(pg * p.c.heads + sg.hk) << p.c.page_log2) + (uint32_t)((key + key_off) & page_mask);
       kv_bulk_load(copy_dst + st * Sh::kStage, copy_src + vec * vec_bytes, copy_bytes, bar + 8 * st);
     }
   };
   uint32_t seq_no = 0;  // stages this warp has used
-  int pg_next = -1;
+  int pg_next = kNoPage;
   uint4 q_raw[Sh::kRowsPerWarp];
   // the first units' copies and the query rows of a segment are on their way
   // before the previous one's results are joined
   const int wj = lane % NB, wi = lane / NB;  // the word of a query row this lane prepares
   auto begin = [&] {
+    table = p.table + (int64_t)sg.b * p.table_stride;
     int pg[Sh::kStages];
 #pragma unroll
     for (int s = 0; s < Sh::kStages; ++s) pg[s] = page_of(sg.key0 + (warp + s * kKvWarps) * kKvUnit);
@@ -542,11 +626,16 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane == 0) s_qs[j][r] = s * 5.9604644775390625e-08f;  // 2^-24, as the codes
       }
-      if (lane == 0) s_hf[r] = ldexpf(p.scale * kLog2e, 24 - 14 + ex);
+      if (lane == 0) {
+        const int i = (sg.r0 + r) / group;
+        s_hf[r] = ldexpf(p.scale * kLog2e, 24 - 14 + ex);
+        s_hi[r] = sg.hi(p, i), s_lo[r] = sg.lo(p, i);
+      }
     }
     __syncthreads();
 
     KvRun<D, B, NT> acc;
+    acc.pending = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -554,10 +643,8 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
         const int r = 8 * n + 2 * t + e;
         acc.hf[n][e] = s_hf[r];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) acc.qs[n][j][e] = s_qs[j][r], acc.zs[n][j][e] = 0.0f;
+        for (int j = 0; j < NB; ++j) acc.qs[n][j][e] = s_qs[j][r], acc.zs[n][j][e] = acc.zs[n][j][2 + e] = 0.0f;
         acc.m[n][e] = -INFINITY, acc.l[n][e] = 0.0f;
-        const int i = (sg.r0 + r) / group;
-        acc.hi[n][e] = sg.hi(p, i), acc.lo[n][e] = sg.lo(p, i);
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -571,10 +658,9 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
       if (!mbar_wait(bar + 8 * st, (seq_no / Sh::kStages) & 1, p.status, &s_abort, p.wait_ns)) break;
       const uint32_t parts = (there >> (2 * st)) & 3u;
       const uint8_t *kc = ring + st * Sh::kStage;
-      if (key >= sg.lo_all && key + kKvUnit <= sg.hi_all && parts == (part_log2 == 5 ? 1u : 3u))
-        kv_unit<D, B, NT, false>(acc, kc, s_q, key, lane, sg.hi_any, sg.lo_any, parts, part_log2);
-      else
-        kv_unit<D, B, NT, true>(acc, kc, s_q, key, lane, sg.hi_any, sg.lo_any, parts, part_log2);
+      const bool inside = key >= sg.lo_all && key + kKvUnit <= sg.hi_all && parts == (part_log2 == 5 ? 1u : 3u);
+      if (inside) kv_unit<D, B, NT, true>(acc, kc, s_q, s_hi, s_lo, key, lane, k == warp, sg.hi_any, sg.lo_any, parts, part_log2);
+      else kv_unit<D, B, NT, false>(acc, kc, s_q, s_hi, s_lo, key, lane, k == warp, sg.hi_any, sg.lo_any, parts, part_log2);
       __syncwarp();  // the stage has been read
       if (k + Sh::kStages * kKvWarps < sg.count) issue(key + Sh::kStages * kKvWarps * kKvUnit, pg_next, seq_no + Sh::kStages);
       pg_next = page_of(key + (Sh::kStages + 1) * kKvWarps * kKvUnit);
@@ -591,11 +677,7 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          acc.l[n][e] += __shfl_xor_sync(0xffffffffu, acc.l[n][e], o);
-#pragma unroll
-          for (int j = 0; j < NB; ++j) acc.zs[n][j][e] += __shfl_xor_sync(0xffffffffu, acc.zs[n][j][e], o);
-        }
+        for (int o = 4; o < 32; o <<= 1) acc.l[n][e] += __shfl_xor_sync(0xffffffffu, acc.l[n][e], o);
         if (g == 0) {
           s_m[warp * R + 8 * n + 2 * t + e] = acc.m[n][e];
           s_l[warp * R + 8 * n + 2 * t + e] = acc.l[n][e];
@@ -646,7 +728,8 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
     const int units = done.v.units, rows = done.rows;
     const bool whole = done.count == units;
     const int64_t seg0 = done.base + (int64_t)done.seg * done.v.cost;  // the segment's units in the list
-    auto part_of = [&](int cta) { return p.parts + ((int64_t)cta * 2 + (begin_of(cta) < seg0 ? 1 : 0)) * Sh::kPart; };
+    // a run's slot: its first segment, or the one it ends in
+    auto part_of = [&](int cta, bool began_before) { return p.parts + ((int64_t)cta * 2 + (began_before ? 1 : 0)) * Sh::kPart; };
     // row r of the tile, elements d .. d + 3, from the sums o, the maximum and l
     auto finish = [&](int r, int d, float4 o, float m, float l) {
       if (r >= rows) return;
@@ -677,19 +760,17 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
       if (whole) {
         finish(r, d, o, m, l);
       } else {
-        float *part = part_of(c);
+        float *part = part_of(c, begin_of(c) < seg0);
         __stcg(reinterpret_cast<float4 *>(part + r * D + d), o);
         if (d == 0) __stcg(reinterpret_cast<float2 *>(part + R * D) + r, make_float2(m, l));
       }
     }
     if (!whole) {
       // the CTAs of the segment join: counted on the first one's word
-      int c0 = c, c1 = c;
-      while (begin_of(c0) > seg0) --c0;
-      while (begin_of(c1 + 1) < seg0 + units) ++c1;
-      __threadfence();
+      const int c0 = (int)kv_div64((seg0 + 1) * ctas - 1, total), c1 = (int)kv_div64((seg0 + units) * ctas - 1, total);
       __syncthreads();
       if (tid == 0) {
+        __threadfence();  // the CTA's results (ordered by the barrier) before its count
         const unsigned old = atomicAdd(p.counts + c0, 1u);
         s_last = old == (unsigned)(c1 - c0);
         if (s_last) p.counts[c0] = 0u;
@@ -697,38 +778,61 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
       __syncthreads();
       if (s_last) {
         __threadfence();
+        const int n = c1 - c0 + 1;
+        const bool early = begin_of(c0) < seg0;  // only the first can have begun before the segment
+        // a warp for each row: the maximum and sum over the partial results;
+        // their factors go to shared memory (s_o is free)
+        constexpr int kFactors = Sh::kFactors;
+        float *s_f = s_o;
+        for (int r = warp; r < R; r += kKvWarps) {
+          const float *src = part_of(c0, false) + R * D + 2 * r;
+          constexpr int kHold = (Sh::kFactors + 31) / 32;
+          float2 ml[kHold];
+          float m = -INFINITY, l = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kHold; ++i) {
+            const int a = lane + 32 * i;
+            ml[i] = make_float2(-INFINITY, 0.0f);
+            if (a < n) ml[i] = __ldcg(reinterpret_cast<const float2 *>(src + (int64_t)(2 * a + (a == 0 && early ? 1 : 0)) * Sh::kPart));
+            m = fmaxf(m, ml[i].x);
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+          for (int i = 0; i < kHold; ++i) {
+            const int a = lane + 32 * i;
+            const float f = ml[i].x == -INFINITY ? 0.0f : ex2(ml[i].x - m);
+            if (a < n) s_f[r * kFactors + a] = f;
+            l = fmaf(ml[i].y, f, l);
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+          if (lane == 0) s_m[r] = m, s_l[r] = l;
+        }
+        __syncthreads();
         for (int i = tid; i < R * D / 4; i += kKvAttnThreads) {
           const int r = i / (D / 4), d = i % (D / 4) * 4;
           if (r >= rows) continue;
           float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          float m = -INFINITY, l = 0.0f;
-          constexpr int kAhead = 8;  // partial results on their way at once
-          for (int cc = c0; cc <= c1; cc += kAhead) {
+          constexpr int kAhead = 16;  // partial results on their way at once
+          const float *src = part_of(c0, false) + r * D + d;
+          for (int a0 = 0; a0 < n; a0 += kAhead) {
             float4 po[kAhead];
-            float2 ml[kAhead];
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-              const float *part = part_of(min(cc + a, c1));
-              po[a] = __ldcg(reinterpret_cast<const float4 *>(part + r * D + d));
-              ml[a] = __ldcg(reinterpret_cast<const float2 *>(part + R * D) + r);
+              const int k = min(a0 + a, n - 1);
+              po[a] = ldcg_v4(src + (int64_t)(2 * k + (k == 0 && early ? 1 : 0)) * Sh::kPart);
             }
-            float top = m;
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-              if (cc + a <= c1) top = fmaxf(top, ml[a].x);
-            const float f = m == -INFINITY ? 0.0f : ex2(m - top);
-            o.x *= f, o.y *= f, o.z *= f, o.w *= f, l *= f;
-            m = top;
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a)
-              if (cc + a <= c1) {
-                const float fa = ml[a].x == -INFINITY ? 0.0f : ex2(ml[a].x - top);
-                o.x = fmaf(po[a].x, fa, o.x), o.y = fmaf(po[a].y, fa, o.y);
-                o.z = fmaf(po[a].z, fa, o.z), o.w = fmaf(po[a].w, fa, o.w);
-                l = fmaf(ml[a].y, fa, l);
+            for (int a = 0; a < kAhead; ++a) {
+              const float f = a0 + a < n ? s_f[r * kFactors + a0 + a] : 0.0f;
+              if (a0 + a < n) {
+                o.x = fmaf(po[a].x, f, o.x), o.y = fmaf(po[a].y, f, o.y);
+                o.z = fmaf(po[a].z, f, o.z), o.w = fmaf(po[a].w, f, o.w);
               }
+            }
           }
-          finish(r, d, o, m, l);
+          finish(r, d, o, s_m[r], s_l[r]);
         }
       }
     }
