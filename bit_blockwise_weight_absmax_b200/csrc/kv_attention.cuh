@@ -73,7 +73,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnParams &p, int b) {
 
 constexpr int kKvUnit = 32;    // keys per unit
 constexpr int kKvWarps = 8;
-constexpr int kKvSegmentCost = 8;  // of a segment in units of the list, beside its units
+constexpr int kKvSegmentCost = 24;  // of a segment in units of the list, beside its units
 constexpr float kKvMasked = -3.4028235e38f;  // in the place of a score that does not count
 constexpr int kKvAttnThreads = kKvWarps * 32;
 constexpr size_t kKvCountBytes = Q4_WORKSPACE_HEAD;
@@ -487,11 +487,14 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   incl += before;
   if (total == 0) return;
   // all CTAs, or where that leaves less than a unit for each warp, fewer; a
-  // multiple of the segments where there are few: equal ones are then cut
-  // alike, and none lies in two pieces of one CTA
+  // multiple of the segments where there are few and that keeps nearly all
+  // CTAs: equal ones are then cut alike, and none lies in two pieces of a CTA
   const int grid = min((int)gridDim.x, Sh::kFactors);
   int ctas = (int)min((int64_t)grid, (total + kKvWarps - 1) / kKvWarps);
-  if (segs <= grid) ctas = segs * (int)min((int64_t)(grid / segs), kv_div(total + kKvWarps * segs - 1, kKvWarps * segs));
+  if (segs <= grid) {
+    const int each = (int)min((int64_t)(grid / segs), kv_div(total + kKvWarps * segs - 1, kKvWarps * segs));
+    if (each * segs * 16 >= grid * 15 || ctas < grid) ctas = each * segs;
+  }
   const int c = blockIdx.x;
   if (c >= ctas) return;
   auto begin_of = [&](int cta) { return kv_div(total * cta, ctas); };
