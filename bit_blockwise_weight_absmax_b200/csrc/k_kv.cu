@@ -1,5 +1,7 @@
 // k_kv.cu -- launchers of the 4-bit key/value cache kernels.
 #include "q4_internal.h"
+#include <algorithm>
+
 #include "serve_internal.h"
 
 namespace q4 {
@@ -47,11 +49,25 @@ int go_attend(const KvAttnParams &p, int sms, cudaStream_t st) {
   launch_pdl(kern, dim3((unsigned)(Sh::kCtas * sms)), dim3(kKvAttnThreads), Sh::kSmem, st, p);
   return launched();
 }
+// Many rows: a CTA for each 256 rows of a sequence and kv head; the grid is
+// what the rows can make at most (the CTAs past the last tile end at once).
+template <int DT, int D, int B>
+int go_prompt(const KvAttnParams &p, cudaStream_t st) {
+  constexpr auto kern = kv_prompt_kernel<DT, D, B>;
+  const int rc = set_smem_attr_once<kern>(KpShape<D>::kSmem, true);
+  if (rc != Q4_OK) return rc;
+  const int64_t rows = (int64_t)p.total_q * (p.q_heads / p.c.heads);
+  const int64_t tiles = (rows / kKpRows + std::min<int64_t>(p.batch, rows)) * p.c.heads;
+  if (tiles > INT32_MAX) return Q4_ERR_SHAPE;
+  launch_pdl(kern, dim3((unsigned)tiles), dim3(kKpThreads), KpShape<D>::kSmem, st, p);
+  return launched();
+}
 struct Attend {
   const KvAttnParams &p;
   int rows, sms;
   cudaStream_t st;
   template <int DT, int D, int B> int operator()() const {
+    if (rows > 16) return go_prompt<DT, D, B>(p, st);
     return rows <= 8 ? go_attend<DT, D, B, 1>(p, sms, st) : go_attend<DT, D, B, 2>(p, sms, st);
   }
 };
@@ -63,7 +79,7 @@ int run_kv_dequantize(int dt, int D, int B, const KvDequantParams &p, cudaStream
 }
 int run_kv_attention(int dt, int D, int B, const KvAttnParams &p, int64_t max_q, int sms, cudaStream_t st) {
   const int64_t rows = max_q * (p.q_heads / p.c.heads);
-  return by_format(dt, D, B, Attend{p, rows <= 8 ? 8 : 16, sms, st});
+  return by_format(dt, D, B, Attend{p, rows <= 8 ? 8 : rows <= 64 ? 16 : 256, sms, st});
 }
 size_t kv_attention_ws(int D, int sms) {
   return kKvCountBytes + (size_t)2 * sms * 2 * 16 * (D + 2) * sizeof(float);

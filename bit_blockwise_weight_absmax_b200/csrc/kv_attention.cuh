@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   constexpr int NB = Sh::NB, R = Sh::R;
   constexpr int MT = D / 16;  // 16-row tiles of the output's d
   pdl_launch_dependents();
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *s_q = smem + Sh::kRing;
   float *s_o = reinterpret_cast<float *>(s_q + R * Sh::kQRow);  // [4][R][kORow], then [R][kFactors]
   float *s_m = s_o + R * Sh::kFactors, *s_l = s_m + kKvWarps * R;

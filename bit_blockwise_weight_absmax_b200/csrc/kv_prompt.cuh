@@ -1,0 +1,513 @@
+// kv_prompt.cuh -- softmax(scale Q K^T) V over the paged 4-bit cache for many
+// query rows (prompts, chunks of prompts) on tcgen05 tensor cores (sm_100a).
+//
+// Bound by the tensor pipe (4 D flops a row and key) and, as close, by the
+// exponentials (16 a cycle and SM) and by issue.  One CTA per SM takes 256
+// query rows of one sequence and kv head (rows of all the query heads that
+// share it: row = token * group + head) against key tiles of 128:
+//   warps 0..7    softmax: a thread owns a row.  It reads its 128 scores from
+//                 tensor memory, takes the maximum, writes the weights back in
+//                 binary16 over the scores, and rescales the output when the
+//                 maximum has grown by more than 2^8 (seldom);
+//   warps 8..11   dequantize: a thread owns a key.  Codes come straight from
+//                 global memory into registers, a tile ahead; 1024 + code is
+//                 one masked OR, minus 1024 + z exact, times s rounded once to
+//                 binary16, stored in the 128B-swizzled layouts the MMAs read
+//                 (keys K-major, values MN-major).  The order of d inside a
+//                 word follows the nibbles; queries are stored alike, outputs
+//                 put back at the end;
+//   warp 12       issues S = Q K^T (both operands in shared memory) and
+//                 O += P V (weights from tensor memory) for the two 128-row
+//                 halves in turn: while one half's softmax runs, the other's
+//                 products do.
+// Tensor memory: two score tiles of 128 columns (weights over their first 64)
+// and two outputs of D.  Query rows are scaled by a power of two into binary16.
+#pragma once
+#include "kv_attention.cuh"
+
+namespace q4 {
+
+constexpr int kKpRows = 256;   // query rows of a CTA
+constexpr int kKpKeys = 128;   // keys of a tile
+constexpr int kKpThreads = 512;
+constexpr float kKpSlack = 8.0f;
+
+template <int D> struct KpShape {
+  static constexpr int kHalves = D / 64;                       // 128-byte wide parts of a row
+  static constexpr int kTile = kHalves * kKpKeys * 128;        // a key or value tile, also 128 query rows
+  static constexpr int kSmem = 2 * kTile + 4 * kTile + 1024;   // queries, two stages of keys and values
+};
+
+// 32 columns of this warp's 32 lanes of tensor memory, without waiting.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D (tensor memory) = A (tensor memory, 16-bit pairs) . B (shared memory) [+ D]
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// MN-major operand with 128-byte swizzle: rows of k, 64 elements of n (128
+// bytes) each; 8 rows of k are 1024 bytes (stride byte offset), the next 64 n
+// lie `lbo` bytes on (leading byte offset).
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+constexpr uint32_t kUmmaTransposeB = 1u << 16;
+
+// Eight codes of a word as binary16 s (code - z), pairs in the order of the
+// nibbles 04 15 26 37.  z64 = -(64 + z), z1024 = -(1024 + z), both pairs.
+__device__ __forceinline__ uint4 kv_word(uint32_t w, __half2 s, __half2 z64, __half2 z1024) {
+  const __half2 sixteenth = __half2half2(__ushort_as_half(0x2C00));  // 1 / 16
+  auto h2 = [](uint32_t v) { return *reinterpret_cast<__half2 *>(&v); };
+  auto u2 = [](__half2 v) { return *reinterpret_cast<uint32_t *>(&v); };
+  const uint32_t w8 = w >> 8;
+  uint4 r;
+  r.x = u2(__hmul2(__hadd2(h2((w & 0x000F000Fu) | 0x64006400u), z1024), s));
+  r.y = u2(__hmul2(__hfma2(h2((w & 0x00F000F0u) | 0x64006400u), sixteenth, z64), s));
+  r.z = u2(__hmul2(__hadd2(h2((w8 & 0x000F000Fu) | 0x64006400u), z1024), s));
+  r.w = u2(__hmul2(__hfma2(h2((w8 & 0x00F000F0u) | 0x64006400u), sixteenth, z64), s));
+  return r;
+}
+
+template <int DT, int D, int B>
+__global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_constant__ KvAttnParams p) {
+  using Sh = KpShape<D>;
+  constexpr int NB = D / B, W = D / 8;  // words of a vector
+  pdl_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t *s_qt = smem;                  // [2 halves of rows][kTile]
+  uint8_t *s_kv = smem + 2 * Sh::kTile;  // [2 stages][keys, values][kTile]
+  __shared__ uint64_t s_bar[14];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_where[4];
+  __shared__ int64_t s_scan[kKpThreads / 32];
+  __shared__ uint4 s_bad[4];  // keys of a tile that no row may read
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bar0 = smem_u32(s_bar);
+  auto k_full = [&](int s) { return bar0 + 8u * s; };
+  auto k_empty = [&](int s) { return bar0 + 8u * (2 + s); };
+  auto v_full = [&](int s) { return bar0 + 8u * (4 + s); };
+  auto v_empty = [&](int s) { return bar0 + 8u * (6 + s); };
+  auto s_full = [&](int h) { return bar0 + 8u * (8 + h); };
+  auto p_full = [&](int h) { return bar0 + 8u * (10 + h); };
+  auto pv_done = [&](int h) { return bar0 + 8u * (12 + h); };
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(k_full(s), 4);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), 4);
+      mbar_init(v_empty(s), 1);
+      mbar_init(s_full(s), 1);
+      mbar_init(p_full(s), 4);
+      mbar_init(pv_done(s), 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_abort = 0;
+    s_where[0] = -1;
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  // this CTA's tile: a prefix sum over the sequences' (row tile, kv head)
+  // tiles, heads fastest, a sequence's last rows (the longest) first
+  const int group = p.q_heads / p.c.heads;
+  const int per = (p.batch + kKpThreads - 1) / kKpThreads;
+  auto tiles_of = [&](int b) -> int64_t {
+    const KvSeq s = kv_seq(p, b);
+    return ((int64_t)s.n * group + kKpRows - 1) / kKpRows * p.c.heads;
+  };
+  int64_t mine = 0;
+  for (int b = tid * per; b < min(p.batch, (tid + 1) * per); ++b) mine += tiles_of(b);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) incl += s_scan[w];
+  const int64_t x = blockIdx.x;
+  if (x >= incl - mine && x < incl) {
+    int64_t at = incl - mine;
+    int b = tid * per;
+    while (x >= at + tiles_of(b)) at += tiles_of(b++);
+    const int rt = (int)(tiles_of(b) / p.c.heads);
+    s_where[0] = b;
+    s_where[1] = (rt - 1 - (int)((x - at) / p.c.heads)) * kKpRows;
+    s_where[2] = (int)((x - at) % p.c.heads);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int b = s_where[0], r0 = s_where[1], hk = s_where[2];
+  volatile int *abort = &s_abort;
+  KvSeq sq = {0, 0, 0};
+  int rows = 0, tiles = 0, tile0 = 0, lo_first = 0, hi_last = 0;
+  if (b >= 0) {
+    sq = kv_seq(p, b);
+    rows = min(kKpRows, sq.n * group - r0);
+    const int p0 = sq.len - sq.n, i0 = r0 / group, i1 = (r0 + rows - 1) / group;
+    lo_first = p.window ? max(0, p0 + i0 - p.window + 1) : 0;
+    hi_last = p.causal ? min(sq.len, p0 + i1 + 1) : sq.len;
+    tile0 = lo_first / kKpKeys;
+    tiles = max(0, (hi_last + kKpKeys - 1) / kKpKeys - tile0);
+  }
+  const uint32_t s_addr = tmem, o_addr = tmem + 256;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int half = warp >> 2;
+    const int rl = tid & 127;                 // row within the half: its lane of tensor memory
+    const int r = half * 128 + rl, row = r0 + r;
+    const bool real = r < rows;
+    const int i = row / group, h = hk * group + row % group;
+    const int p0 = sq.len - sq.n;
+    const int hi = p.causal ? min(sq.len, p0 + i + 1) : sq.len, lo = p.window ? max(0, p0 + i - p.window + 1) : 0;
+    float hf = 0.0f;
+    // the query row: scaled into binary16, words in the cache's order, nibble
+    // order within a word
+    {
+      const uint16_t *q = p.Q + (int64_t)(sq.q0 + i) * p.q_ts + (int64_t)h * p.q_hs;
+      float top = 0.0f;
+      uint4 raw[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        raw[w] = make_uint4(0, 0, 0, 0);
+        if (real) raw[w] = __ldcg(reinterpret_cast<const uint4 *>(q + (w % NB) * B + 8 * (w / NB)));
+        const uint32_t u[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(lo16<DT>(u[e])), fabsf(hi16<DT>(u[e]))));
+      }
+      const int ex = top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127, -110) : 0;
+      // 2^(14 - ex), with the scale's sign: scores then grow with the products
+      const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - ex) << 23), p.scale);
+      hf = fmaxf(ldexpf(fabsf(p.scale) * 1.4426950408889634f, ex - 14), 1e-37f);
+      uint8_t *dst = s_qt + half * Sh::kTile + rl * 128;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const uint32_t u[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[2 * e] = lo16<DT>(u[e]) * up, f[2 * e + 1] = hi16<DT>(u[e]) * up;
+        uint4 o;
+        o.x = Dt<Q4_F16>::pack2(f[0], f[4]);
+        o.y = Dt<Q4_F16>::pack2(f[1], f[5]);
+        o.z = Dt<Q4_F16>::pack2(f[2], f[6]);
+        o.w = Dt<Q4_F16>::pack2(f[3], f[7]);
+        *reinterpret_cast<uint4 *>(dst + (w >> 3) * (kKpKeys * 128) + (((w & 7) ^ (rl & 7)) << 4)) = o;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(half));  // its first phase: the queries are there
+    }
+    const uint32_t st = s_addr + (uint32_t)(half * 128) + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ot = o_addr + (uint32_t)(half * D) + ((uint32_t)((warp & 3) * 32) << 16);
+    float m = -INFINITY, l = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < tiles; ++j) {
+      if (!mbar_wait_warp(s_full(half), j & 1, p.status, abort, p.wait_ns)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int key0 = (tile0 + j) * kKpKeys;
+      const uint4 bad = s_bad[j & 3];
+      const bool masked = __any_sync(0xffffffffu, key0 < lo || key0 + kKpKeys > hi || (bad.x | bad.y | bad.z | bad.w) != 0);
+      uint32_t s[64];  // half of the scores at a time
+      auto load = [&](int k0) {
+        tmem_ld32(st + k0, s);
+        tmem_ld32(st + k0 + 32, s + 32);
+        tmem_wait_ld();
+        if (masked) {
+          const uint32_t bw[2] = {k0 ? bad.z : bad.x, k0 ? bad.w : bad.y};
+          const int from = lo - key0 - k0, to = hi - key0 - k0;
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (k < from || k >= to || ((bw[k >> 5] >> (k & 31)) & 1u)) s[k] = 0xFF800000u;  // -inf
+        }
+      };
+      float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto take_max = [&] {
+#pragma unroll
+        for (int k = 0; k < 64; k += 8) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            top4[e] = fmaxf(top4[e], fmaxf(__uint_as_float(s[k + e]), __uint_as_float(s[k + 4 + e])));
+        }
+      };
+      load(64);
+      take_max();
+      load(0);
+      take_max();
+      const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * hf;
+      float f = 1.0f;
+      if (top > m + kKpSlack) {
+        f = m == -INFINITY ? 0.0f : ex2(m - top);
+        m = top;
+        l *= f;
+      }
+      if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+        // the output so far takes the new reference, once its last product is in
+        if (!mbar_wait_warp(pv_done(half), (j - 1) & 1, p.status, abort, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          tmem_ld16(ot + 16 * c, o);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+          tmem_st16(ot + 16 * c, o);
+        }
+        tmem_wait_st();
+      }
+      const float mm = m == -INFINITY ? 0.0f : -m;
+      const uint64_t hf2 = f2_pack(hf, hf), mm2 = f2_pack(mm, mm);
+      uint64_t l2[2] = {0, 0};  // two packed sums
+      // the first half is at hand; its weights lie over scores that are read,
+      // and so do the second half's once that has been loaded again
+      auto weigh = [&](int k0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float a, e;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1])), hf2, mm2), a, e);
+            a = ex2(a), e = ex2(e);
+            l2[k & 1] = f2_add(l2[k & 1], f2_pack(a, e));
+            w[k] = Dt<Q4_F16>::pack2(a, e);
+          }
+          tmem_st16(st + k0 / 2 + 16 * c, w);
+        }
+      };
+      weigh(0);
+      load(64);
+      weigh(64);
+      {
+        float a, e;
+        f2_unpack(f2_add(l2[0], l2[1]), a, e);
+        l += a + e;
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full(half));
+    }
+    // ---- the row's output ----
+    if (ok && tiles > 0) ok = mbar_wait_warp(pv_done(half), (tiles - 1) & 1, p.status, abort, p.wait_ns);
+    if (ok && b >= 0) {
+      tc_fence_after();
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int64_t at = (int64_t)(sq.q0 + i) * p.q_heads + h;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (tiles > 0) {
+          tmem_ld32(ot + 32 * c, o);
+          tmem_wait_ld();
+        }
+        if (!real) continue;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {  // word 4 c + v of the row
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = l == 0.0f ? 0.0f : __uint_as_float(o[8 * v + e]) * inv;
+          const int w = 4 * c + v;
+          uint4 out;
+          out.x = Dt<DT>::pack2(f[0], f[2]);
+          out.y = Dt<DT>::pack2(f[4], f[6]);
+          out.z = Dt<DT>::pack2(f[1], f[3]);
+          out.w = Dt<DT>::pack2(f[5], f[7]);
+          *reinterpret_cast<uint4 *>(p.out + at * D + (w % NB) * B + 8 * (w / NB)) = out;
+        }
+      }
+      if (real && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m + __log2f(l)) * 0.69314718055994531f;
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ dequantize
+    const int kk = tid - 256;  // key of a tile
+    const int pages = (int)(p.c.slots >> p.c.page_log2), page_mask = (1 << p.c.page_log2) - 1;
+    const int32_t *table = b >= 0 ? p.table + (int64_t)b * p.table_stride : nullptr;
+    constexpr int kNone = INT_MIN;
+    auto page_of = [&](int j) -> int {  // table entry of this thread's key of tile j
+      const int key = (tile0 + j) * kKpKeys + kk;
+      if (j >= tiles || key >= hi_last || key < lo_first) return kNone;
+      return __ldg(table + (key >> p.c.page_log2));
+    };
+    constexpr int V4 = D / 32;
+    uint4 raw[2][V4];      // codes of the key and of the value
+    uint32_t state[2][NB];
+    bool bad_page = false, there = false;
+    auto load = [&](int j, int pg) {
+      const int key = (tile0 + j) * kKpKeys + kk;
+      there = pg >= 0 && pg < pages;
+      bad_page = !there && pg != kNone;
+      if (bad_page) raise_status(p.status, Q4_STATUS_INDEX);
+      const int64_t vec = ((((int64_t)(there ? pg : 0) * p.c.heads) + hk) << p.c.page_log2) + (key & page_mask);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int v = 0; v < V4; ++v)
+          raw[w][v] = there ? __ldg(reinterpret_cast<const uint4 *>(p.c.codes[w] + vec * (D / 2)) + v) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) state[w][n] = there ? __ldg(p.c.state[w] + vec * NB + n) : 0u;
+      }
+    };
+    auto store = [&](int which, int stage, bool poison) {
+      uint8_t *dst = s_kv + (stage * 2 + which) * Sh::kTile + kk * 128;
+      __half2 s[NB], z64[NB], z1024[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const __half2 sz = *reinterpret_cast<const __half2 *>(&state[which][n]);
+        s[n] = __low2half2(sz);
+        if (poison) s[n] = __half2half2(__ushort_as_half(which == 0 ? 0x7FFF : 0));
+        const __half2 z = __high2half2(sz);
+        z64[n] = __hsub2(__half2half2(__ushort_as_half(0xD400)), z);    // -64 - z
+        z1024[n] = __hsub2(__half2half2(__ushort_as_half(0xE400)), z);  // -1024 - z
+      }
+#pragma unroll
+      for (int v = 0; v < V4; ++v) {
+        const uint32_t w4[4] = {raw[which][v].x, raw[which][v].y, raw[which][v].z, raw[which][v].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int w = 4 * v + e, n = w % NB;
+          *reinterpret_cast<uint4 *>(dst + (w >> 3) * (kKpKeys * 128) + (((w & 7) ^ (kk & 7)) << 4)) =
+              kv_word(w4[e], s[n], z64[n], z1024[n]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    load(0, page_of(0));
+    int pg_next = page_of(1);
+    for (int j = 0; j < tiles; ++j) {
+      const int st = j & 1;
+      // a value that is not finite must not meet the zero weights of rows that
+      // do not attend to it: it becomes zero, and its key NaN, so that the rows
+      // that do attend give NaN
+      bool poison = false;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) poison |= (state[1][n] & 0x7C00u) == 0x7C00u;
+      const uint32_t bad = __ballot_sync(0xffffffffu, bad_page);
+      if (lane == 0) reinterpret_cast<uint32_t *>(&s_bad[j & 3])[warp - 8] = bad;
+      if (!mbar_wait_warp(k_empty(st), ((j >> 1) & 1) ^ 1, p.status, abort, p.wait_ns)) break;
+      store(0, st, poison);
+      if (lane == 0) mbar_arrive(k_full(st));
+      if (!mbar_wait_warp(v_empty(st), ((j >> 1) & 1) ^ 1, p.status, abort, p.wait_ns)) break;
+      store(1, st, poison);
+      if (lane == 0) mbar_arrive(v_full(st));
+      if (j + 1 < tiles) load(j + 1, pg_next);
+      pg_next = page_of(j + 2);
+    }
+  } else {
+    if (warp == 12 && lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t id_s = umma_idesc_f16(0, 128, kKpKeys);
+      constexpr uint32_t id_o = umma_idesc_f16(0, 128, D) | kUmmaTransposeB;
+      const uint32_t q0 = smem_u32(s_qt), kv0 = smem_u32(s_kv);
+      auto scores = [&](int half, int st) {
+        const uint32_t a0 = q0 + half * Sh::kTile, b0 = kv0 + (st * 2) * Sh::kTile;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * (kKpKeys * 128) + (k & 3) * 32;
+          umma_f16(s_addr + half * 128, umma_desc_sw128(a0 + off), umma_desc_sw128(b0 + off), id_s, k != 0);
+        }
+      };
+      auto output = [&](int half, int st, bool first) {
+        const uint32_t b0 = kv0 + (st * 2 + 1) * Sh::kTile;
+#pragma unroll
+        for (int k = 0; k < kKpKeys / 16; ++k)
+          umma_f16_ts(o_addr + half * D, s_addr + half * 128 + 8 * k, umma_desc_mn_sw128(b0 + 2048 * k, kKpKeys * 128), id_o,
+                      !first || k != 0);
+      };
+      auto wait = [&](uint32_t bar, uint32_t par) {
+        const bool ok = mbar_wait(bar, par, p.status, abort, p.wait_ns);
+        tc_fence_after();
+        return ok;
+      };
+      bool ok = true;
+      uint32_t last_bar = 0, last_par = 0;
+      bool committed = false;
+      auto commit = [&](uint32_t bar, uint32_t par) {
+        umma_commit(bar);
+        last_bar = bar, last_par = par, committed = true;
+      };
+      if (tiles > 0) {
+        ok = wait(p_full(0), 0) && wait(p_full(1), 0) && wait(k_full(0), 0);  // queries, first keys
+        if (ok) {
+          scores(0, 0);
+          commit(s_full(0), 0);
+          scores(1, 0);
+          commit(s_full(1), 0);
+          commit(k_empty(0), 0);
+        }
+      }
+      for (int j = 0; j < tiles && ok; ++j) {
+        const int st = j & 1, nx = (j + 1) & 1;
+        for (int half = 0; half < 2 && ok; ++half) {
+          // phase j + 1 of the weights (phase 0 was the queries)
+          ok = wait(p_full(half), (j + 1) & 1) && (half || wait(v_full(st), (j >> 1) & 1));
+          if (!ok) break;
+          output(half, st, j == 0);
+          commit(pv_done(half), j & 1);
+          if (half) commit(v_empty(st), (j >> 1) & 1);
+          if (j + 1 < tiles) {
+            ok = half || wait(k_full(nx), ((j + 1) >> 1) & 1);
+            if (!ok) break;
+            scores(half, nx);
+            commit(s_full(half), (j + 1) & 1);
+            if (half) commit(k_empty(nx), ((j + 1) >> 1) & 1);
+          }
+        }
+      }
+      // every MMA issued completes before TMEM is freed, also after a timeout
+      if (committed) {
+        int dummy = 0;
+        volatile int no_abort = 0;
+        mbar_wait(last_bar, last_par, &dummy, &no_abort);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+}  // namespace q4

@@ -6,6 +6,7 @@
 #include "int8_quantize.cuh"
 #include "kv_attention.cuh"
 #include "kv_cache.cuh"
+#include "kv_prompt.cuh"
 
 namespace q4 {
 struct I8Operands {
