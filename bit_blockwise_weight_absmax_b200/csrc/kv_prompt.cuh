@@ -6,9 +6,11 @@
 // query rows of one sequence and kv head (rows of all the query heads that
 // share it: row = token * group + head) against key tiles of 128:
 //   warps 0..7    softmax: a thread owns a row.  It reads its 128 scores from
-//                 tensor memory, takes the maximum, writes the weights back in
-//                 binary16 over the scores, and rescales the output when the
-//                 maximum has grown by more than 2^14 (seldom);
+//                 tensor memory and writes the weights back in binary16 over
+//                 them.  The reference m of 2^(score - m) stays that of earlier
+//                 tiles while the weights fit binary16 (their sum tells); only
+//                 then, and for the first tile, the maximum is taken and the
+//                 output rescaled: one pass over the scores in the common case;
 //   warps 8..11   dequantize: a thread owns a key.  Codes come straight from
 //                 global memory into registers, a tile ahead; 1024 + code is
 //                 one masked OR, minus 1024 + z exact, times s rounded once to
@@ -30,7 +32,7 @@ namespace q4 {
 constexpr int kKpRows = 256;   // query rows of a CTA
 constexpr int kKpKeys = 128;   // keys of a tile
 constexpr int kKpThreads = 512;
-constexpr float kKpSlack = 14.0f;  // weights stay below 2^15: inside binary16
+constexpr float kKpMost = 32768.0f;  // of a row's weights in a tile: each is inside binary16 then
 
 template <int D> struct KpShape {
   static constexpr int kHalves = D / 64;                       // 128-byte wide parts of a row
@@ -208,6 +210,8 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
+    // 2 x 176 + 96 + 64 = 4 x 128 registers: what the block was launched with
+    
     const int half = warp >> 2;
     const int rl = tid & 127;                 // row within the half: its lane of tensor memory
     const int r = half * 128 + rl, row = r0 + r;
@@ -257,92 +261,91 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int j = 0; j < tiles; ++j) {
-      if (!mbar_wait_warp(s_full(half), j & 1, p.status, abort, p.wait_ns)) {
+      if (!mbar_wait(s_full(half), j & 1, p.status, abort, p.wait_ns)) {
         ok = false;
         break;
       }
+      __syncwarp();
       tc_fence_after();
       const int key0 = (tile0 + j) * kKpKeys;
       const uint4 bad = s_bad[j & 3];
       const bool masked = __any_sync(0xffffffffu, key0 < lo || key0 + kKpKeys > hi || (bad.x | bad.y | bad.z | bad.w) != 0);
-      uint32_t s[64];  // half of the scores at a time
-      auto load = [&](int k0) {
-        tmem_ld32(st + k0, s);
-        tmem_ld32(st + k0 + 32, s + 32);
-        tmem_wait_ld();
-        if (masked) {
-          const uint32_t bw[2] = {k0 ? bad.z : bad.x, k0 ? bad.w : bad.y};
-          const int from = lo - key0 - k0, to = hi - key0 - k0;
+      auto mask = [&](uint32_t *s, int c) {  // scores 32 c .. of the tile
+        const uint32_t bw = c == 0 ? bad.x : c == 1 ? bad.y : c == 2 ? bad.z : bad.w;
+        const int from = lo - key0 - 32 * c, to = hi - key0 - 32 * c;
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (k < from || k >= to || ((bw[k >> 5] >> (k & 31)) & 1u)) s[k] = 0xFF800000u;  // -inf
-        }
+        for (int k = 0; k < 32; ++k)
+          if (k < from || k >= to || ((bw >> k) & 1u)) s[k] = 0xFF800000u;  // -inf
       };
-      float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto take_max = [&] {
+      uint32_t w[64];  // the weights, pairs of keys
+      float sum = 0.0f;
+      auto weigh = [&] {
+        const float mm = m == -INFINITY ? 0.0f : -m;
+        const uint64_t hf2 = f2_pack(hf, hf), mm2 = f2_pack(mm, mm);
+        uint64_t l2[2] = {0, 0};  // two packed sums
+        uint32_t s[2][32];        // the next 32 scores are on their way
+        tmem_ld32(st, s[0]);
 #pragma unroll
-        for (int k = 0; k < 64; k += 8) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            top4[e] = fmaxf(top4[e], fmaxf(__uint_as_float(s[k + e]), __uint_as_float(s[k + 4 + e])));
-        }
-      };
-      load(64);
-      take_max();
-      load(0);
-      take_max();
-      const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * hf;
-      float f = 1.0f;
-      if (top > m + kKpSlack) {
-        f = m == -INFINITY ? 0.0f : ex2(m - top);
-        m = top;
-        l *= f;
-      }
-      if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-        // the output so far takes the new reference, once its last product is in
-        if (!mbar_wait_warp(pv_done(half), (j - 1) & 1, p.status, abort, p.wait_ns)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t o[16];
-          tmem_ld16(ot + 16 * c, o);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-          tmem_st16(ot + 16 * c, o);
-        }
-        tmem_wait_st();
-      }
-      const float mm = m == -INFINITY ? 0.0f : -m;
-      const uint64_t hf2 = f2_pack(hf, hf), mm2 = f2_pack(mm, mm);
-      uint64_t l2[2] = {0, 0};  // two packed sums
-      // the first half is at hand; its weights lie over scores that are read,
-      // and so do the second half's once that has been loaded again
-      auto weigh = [&](int k0) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[16];
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld();
+          if (c < 3) tmem_ld32(st + 32 * (c + 1), s[(c + 1) & 1]);
+          if (masked) mask(s[c & 1], c);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            float a, e;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1])), hf2, mm2), a, e);
-            a = ex2(a), e = ex2(e);
-            l2[k & 1] = f2_add(l2[k & 1], f2_pack(a, e));
-            w[k] = Dt<Q4_F16>::pack2(a, e);
+            float x, y;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c & 1][2 * k]), __uint_as_float(s[c & 1][2 * k + 1])), hf2, mm2), x, y);
+            x = ex2(x), y = ex2(y);
+            l2[k & 1] = f2_add(l2[k & 1], f2_pack(x, y));
+            w[16 * c + k] = Dt<Q4_F16>::pack2(x, y);
           }
-          tmem_st16(st + k0 / 2 + 16 * c, w);
         }
+        float x, y;
+        f2_unpack(f2_add(l2[0], l2[1]), x, y);
+        sum = x + y;
       };
-      weigh(0);
-      load(64);
-      weigh(64);
-      {
-        float a, e;
-        f2_unpack(f2_add(l2[0], l2[1]), a, e);
-        l += a + e;
+      // the reference of the tiles before serves as long as no weight leaves
+      // binary16, which the row's sum of weights tells; else (and for the
+      // first keys) it moves to the maximum
+      bool move = m == -INFINITY;
+#pragma unroll 1
+      for (int pass = __any_sync(0xffffffffu, move) ? 1 : 0; ok; ++pass) {
+        if (pass) {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s[32];
+            tmem_ld32(st + 32 * c, s);
+            tmem_wait_ld();
+            if (masked) mask(s, c);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(s[k]));
+          }
+          top = fmaxf(m, top * hf);
+          const float f = !move || m == -INFINITY ? 1.0f : ex2(m - top);
+          if (move) m = top, l *= f;
+          if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+            // the output so far takes the new reference, once its last product is in
+            ok = mbar_wait(pv_done(half), (j - 1) & 1, p.status, abort, p.wait_ns);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(ot + 16 * c, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st16(ot + 16 * c, o);
+            }
+          }
+        }
+        weigh();
+        move = !(sum <= kKpMost);
+        if (pass || !__any_sync(0xffffffffu, move)) break;
       }
+      if (!ok) break;
+      l += sum;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_st16(st + 16 * c, w + 16 * c);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -380,6 +383,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ dequantize
+    
     const int kk = tid - 256;  // key of a tile
     const int pages = (int)(p.c.slots >> p.c.page_log2), page_mask = (1 << p.c.page_log2) - 1;
     const int32_t *table = b >= 0 ? p.table + (int64_t)b * p.table_stride : nullptr;
@@ -457,6 +461,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
       pg_next = page_of(j + 2);
     }
   } else {
+    
     if (warp == 12) {
       // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t id_s = umma_idesc_f16(0, 128, kKpKeys);
