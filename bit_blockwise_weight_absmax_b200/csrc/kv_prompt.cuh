@@ -64,19 +64,19 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // descriptors then stay in uniform registers.  (Issued inside a one-lane
 // branch, 32 of them took 3700 cycles for 2048 of tensor work.)
 // D (tensor memory) = A . B (shared memory) [+ D]
-__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t lead) {
   asm volatile(
       "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
       : "memory");
 }
 // D (tensor memory) = A (tensor memory, 16-bit pairs) . B (shared memory) [+ D]
-__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t lead) {
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t lead) {
   asm volatile(
       "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
       : "memory");
 }
 __device__ __forceinline__ void umma_commit_lead(uint32_t bar, uint32_t lead) {
@@ -132,7 +132,10 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
   __shared__ int s_abort, s_where[4];
   __shared__ int64_t s_scan[kKpThreads / 32];
   __shared__ uint4 s_bad[4];  // keys of a tile that no row may read
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // values that are the same in a warp are marked so (a shuffle): the MMA
+  // warp's addresses and control flow then stay in the uniform datapath
+  auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const uint32_t bar0 = smem_u32(s_bar);
   auto k_full = [&](int s) { return bar0 + 8u * s; };
   auto k_empty = [&](int s) { return bar0 + 8u * (2 + s); };
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = (uint32_t)uniform((int)s_tmem);
   const int b = s_where[0], r0 = s_where[1], hk = s_where[2];
   volatile int *abort = &s_abort;
   KvSeq sq = {0, 0, 0};
@@ -206,12 +209,11 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     tile0 = lo_first / kKpKeys;
     tiles = max(0, (hi_last + kKpKeys - 1) / kKpKeys - tile0);
   }
+  tiles = uniform(tiles);
   const uint32_t s_addr = tmem, o_addr = tmem + 256;
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
-    // 2 x 176 + 96 + 64 = 4 x 128 registers: what the block was launched with
-    
     const int half = warp >> 2;
     const int rl = tid & 127;                 // row within the half: its lane of tensor memory
     const int r = half * 128 + rl, row = r0 + r;
