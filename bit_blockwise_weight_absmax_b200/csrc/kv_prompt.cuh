@@ -32,6 +32,7 @@ namespace q4 {
 constexpr int kKpRows = 256;   // query rows of a CTA
 constexpr int kKpKeys = 128;   // keys of a tile
 constexpr int kKpThreads = 512;
+constexpr float kKpAhead = 14.0f;    // scores up to this far past the reference keep it
 constexpr float kKpMost = 32768.0f;  // of a row's weights in a tile: each is inside binary16 then
 
 template <int D> struct KpShape {
@@ -64,19 +65,23 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // descriptors then stay in uniform registers.  (Issued inside a one-lane
 // branch, 32 of them took 3700 cycles for 2048 of tensor work.)
 // D (tensor memory) = A . B (shared memory) [+ D]
-__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t lead) {
+// A descriptor's low word carries the address (16-byte units) and moves by
+// additions; its high word is the same for all operands here (stride byte
+// offset 1024, version 1, 128-byte swizzle).
+constexpr uint32_t kUmmaDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate, uint32_t lead) {
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
+      "{ .reg .pred p, q; .reg .b64 da, db; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; mov.b64 da, {%1, %6}; mov.b64 db, {%2, %6}; "
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead), "n"(kUmmaDescHi)
       : "memory");
 }
 // D (tensor memory) = A (tensor memory, 16-bit pairs) . B (shared memory) [+ D]
-__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t lead) {
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate, uint32_t lead) {
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
+      "{ .reg .pred p, q; .reg .b64 db; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; mov.b64 db, {%2, %6}; "
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead), "n"(kUmmaDescHi)
       : "memory");
 }
 __device__ __forceinline__ void umma_commit_lead(uint32_t bar, uint32_t lead) {
@@ -86,18 +91,11 @@ __device__ __forceinline__ void umma_commit_lead(uint32_t bar, uint32_t lead) {
       "r"(lead)
       : "memory");
 }
-// MN-major operand with 128-byte swizzle: rows of k, 64 elements of n (128
-// bytes) each; 8 rows of k are 1024 bytes (stride byte offset), the next 64 n
-// lie `lbo` bytes on (leading byte offset).
-__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t addr, uint32_t lbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
-}
+// Low words: K-major operands (leading byte offset unused, 1), and MN-major
+// ones: rows of k of 64 elements of n (128 bytes), 8 rows a swizzle atom, the
+// next 64 n `lbo` bytes on (leading byte offset).
+__device__ __forceinline__ uint32_t desc_lo_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_lo_mn(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
 constexpr uint32_t kUmmaTransposeB = 1u << 16;
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
@@ -127,7 +125,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
   uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *s_qt = smem;                  // [2 halves of rows][kTile]
   uint8_t *s_kv = smem + 2 * Sh::kTile;  // [2 stages][keys, values][kTile]
-  __shared__ uint64_t s_bar[14];
+  __shared__ uint64_t s_bar[18];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_where[4];
   __shared__ int64_t s_scan[kKpThreads / 32];
@@ -142,8 +140,11 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
   auto v_full = [&](int s) { return bar0 + 8u * (4 + s); };
   auto v_empty = [&](int s) { return bar0 + 8u * (6 + s); };
   auto s_full = [&](int h) { return bar0 + 8u * (8 + h); };
-  auto p_full = [&](int h) { return bar0 + 8u * (10 + h); };
-  auto pv_done = [&](int h) { return bar0 + 8u * (12 + h); };
+  // the weights of keys 64 u .. of a tile (a barrier each: a warp may be done
+  // with both before another is with the first); the first phase of u = 0 is
+  // the queries'
+  auto p_full = [&](int h, int u) { return bar0 + 8u * (10 + 2 * h + u); };
+  auto pv_done = [&](int h, int u) { return bar0 + 8u * (14 + 2 * h + u); };
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(k_full(s), 4);
@@ -151,8 +152,10 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
       mbar_init(v_full(s), 4);
       mbar_init(v_empty(s), 1);
       mbar_init(s_full(s), 1);
-      mbar_init(p_full(s), 4);
-      mbar_init(pv_done(s), 1);
+      mbar_init(p_full(s, 0), 4);
+      mbar_init(p_full(s, 1), 4);
+      mbar_init(pv_done(s, 0), 1);
+      mbar_init(pv_done(s, 1), 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_abort = 0;
@@ -199,13 +202,16 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
   const int b = s_where[0], r0 = s_where[1], hk = s_where[2];
   volatile int *abort = &s_abort;
   KvSeq sq = {0, 0, 0};
-  int rows = 0, tiles = 0, tile0 = 0, lo_first = 0, hi_last = 0;
+  int rows = 0, tiles = 0, tile0 = 0, lo_first = 0, hi_last = 0;  // keys some row attends to
+  int lo_all = 0, hi_all = 0;                                    // keys all rows do
   if (b >= 0) {
     sq = kv_seq(p, b);
     rows = min(kKpRows, sq.n * group - r0);
     const int p0 = sq.len - sq.n, i0 = r0 / group, i1 = (r0 + rows - 1) / group;
     lo_first = p.window ? max(0, p0 + i0 - p.window + 1) : 0;
     hi_last = p.causal ? min(sq.len, p0 + i1 + 1) : sq.len;
+    lo_all = p.window ? max(0, p0 + i1 - p.window + 1) : 0;
+    hi_all = p.causal ? min(sq.len, p0 + i0 + 1) : sq.len;
     tile0 = lo_first / kKpKeys;
     tiles = max(0, (hi_last + kKpKeys - 1) / kKpKeys - tile0);
   }
@@ -256,13 +262,14 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(half));  // its first phase: the queries are there
+      if (lane == 0) mbar_arrive(p_full(half, 0));
     }
     const uint32_t st = s_addr + (uint32_t)(half * 128) + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ot = o_addr + (uint32_t)(half * D) + ((uint32_t)((warp & 3) * 32) << 16);
     float m = -INFINITY, l = 0.0f;
-    bool ok = true;
-    for (int j = 0; j < tiles; ++j) {
+    const uint64_t hf2 = f2_pack(hf, hf);
+    bool ok = true, fresh = true;  // fresh: a row of the warp has no reference yet
+    for (int j = 0; j < tiles && ok; ++j) {
       if (!mbar_wait(s_full(half), j & 1, p.status, abort, p.wait_ns)) {
         ok = false;
         break;
@@ -270,64 +277,70 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
       __syncwarp();
       tc_fence_after();
       const int key0 = (tile0 + j) * kKpKeys;
-      const uint4 bad = s_bad[j & 3];
-      const bool masked = __any_sync(0xffffffffu, key0 < lo || key0 + kKpKeys > hi || (bad.x | bad.y | bad.z | bad.w) != 0);
-      auto mask = [&](uint32_t *s, int c) {  // scores 32 c .. of the tile
-        const uint32_t bw = c == 0 ? bad.x : c == 1 ? bad.y : c == 2 ? bad.z : bad.w;
-        const int from = lo - key0 - 32 * c, to = hi - key0 - 32 * c;
+      // 64 keys at a time: the first product starts while the second half's
+      // weights are made
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (k < from || k >= to || ((bw >> k) & 1u)) s[k] = 0xFF800000u;  // -inf
-      };
-      uint32_t w[64];  // the weights, pairs of keys
-      float sum = 0.0f;
-      auto weigh = [&] {
-        const float mm = m == -INFINITY ? 0.0f : -m;
-        const uint64_t hf2 = f2_pack(hf, hf), mm2 = f2_pack(mm, mm);
-        uint64_t l2[2] = {0, 0};  // two packed sums
-        uint32_t s[2][32];        // the next 32 scores are on their way
-        tmem_ld32(st, s[0]);
+      for (int u = 0; u < 2; ++u) {
+        uint32_t s[2][32];
+        tmem_ld32(st + 64 * u, s[0]);
+        tmem_ld32(st + 64 * u + 32, s[1]);
+        const uint4 bad4 = s_bad[j & 3];
+        const uint32_t bad[2] = {u ? bad4.z : bad4.x, u ? bad4.w : bad4.y};
+        const bool masked = key0 < lo_all || key0 + kKpKeys > hi_all || (bad[0] | bad[1]) != 0;
+        auto mask = [&] {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait_ld();
-          if (c < 3) tmem_ld32(st + 32 * (c + 1), s[(c + 1) & 1]);
-          if (masked) mask(s[c & 1], c);
+          for (int c = 0; c < 2; ++c) {
+            const int from = lo - key0 - 64 * u - 32 * c, to = hi - key0 - 64 * u - 32 * c;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < 32; ++k)
+              if (k < from || k >= to || ((bad[c] >> k) & 1u)) s[c][k] = 0xFF800000u;  // -inf
+          }
+        };
+        tmem_wait_ld();
+        if (masked) mask();
+        uint32_t w[32];  // the weights, pairs of keys
+        float sum;
+        auto weigh = [&] {
+          const float mm = m == -INFINITY ? 0.0f : -m;
+          const uint64_t mm2 = f2_pack(mm, mm);
+          uint64_t l2[2] = {0, 0};  // two packed sums
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
             float x, y;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c & 1][2 * k]), __uint_as_float(s[c & 1][2 * k + 1])), hf2, mm2), x, y);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k >> 4][2 * (k & 15)]), __uint_as_float(s[k >> 4][2 * (k & 15) + 1])), hf2, mm2), x, y);
             x = ex2(x), y = ex2(y);
             l2[k & 1] = f2_add(l2[k & 1], f2_pack(x, y));
-            w[16 * c + k] = Dt<Q4_F16>::pack2(x, y);
+            w[k] = Dt<Q4_F16>::pack2(x, y);
           }
+          float x, y;
+          f2_unpack(f2_add(l2[0], l2[1]), x, y);
+          sum = x + y;
+        };
+        // the reference of the keys before serves as long as no weight leaves
+        // binary16, which the row's sum of weights tells; else (and for the
+        // first keys) it moves to the maximum
+        bool move = m == -INFINITY;
+        if (!fresh) {
+          weigh();
+          move = !(sum <= kKpMost);
         }
-        float x, y;
-        f2_unpack(f2_add(l2[0], l2[1]), x, y);
-        sum = x + y;
-      };
-      // the reference of the tiles before serves as long as no weight leaves
-      // binary16, which the row's sum of weights tells; else (and for the
-      // first keys) it moves to the maximum
-      bool move = m == -INFINITY;
-#pragma unroll 1
-      for (int pass = __any_sync(0xffffffffu, move) ? 1 : 0; ok; ++pass) {
-        if (pass) {
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t s[32];
-            tmem_ld32(st + 32 * c, s);
+        if (__any_sync(0xffffffffu, move)) {
+          if (!fresh) {  // the scores again: their registers held the exponents
+            tmem_ld32(st + 64 * u, s[0]);
+            tmem_ld32(st + 64 * u + 32, s[1]);
             tmem_wait_ld();
-            if (masked) mask(s, c);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(s[k]));
+            if (masked) mask();
           }
+          float top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 64; ++k) top = fmaxf(top, __uint_as_float(s[k >> 5][k & 31]));
           top = fmaxf(m, top * hf);
+          if (fresh) move = !(top <= m + kKpAhead);
           const float f = !move || m == -INFINITY ? 1.0f : ex2(m - top);
           if (move) m = top, l *= f;
-          if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+          if ((j | u) && __any_sync(0xffffffffu, f != 1.0f)) {
             // the output so far takes the new reference, once its last product is in
-            ok = mbar_wait(pv_done(half), (j - 1) & 1, p.status, abort, p.wait_ns);
+            ok = mbar_wait(pv_done(half, 1 - u), (j - 1 + u) & 1, p.status, abort, p.wait_ns);
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
@@ -339,22 +352,20 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
               tmem_st16(ot + 16 * c, o);
             }
           }
+          weigh();
+          fresh = __any_sync(0xffffffffu, m == -INFINITY);
         }
-        weigh();
-        move = !(sum <= kKpMost);
-        if (pass || !__any_sync(0xffffffffu, move)) break;
+        l += sum;
+        tmem_st16(st + 32 * u, w);
+        tmem_st16(st + 32 * u + 16, w + 16);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(half, u));
       }
-      if (!ok) break;
-      l += sum;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_st16(st + 16 * c, w + 16 * c);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(half));
     }
     // ---- the row's output ----
-    if (ok && tiles > 0) ok = mbar_wait_warp(pv_done(half), (tiles - 1) & 1, p.status, abort, p.wait_ns);
+    if (ok && tiles > 0) ok = mbar_wait_warp(pv_done(half, 1), (tiles - 1) & 1, p.status, abort, p.wait_ns);
     if (ok && b >= 0) {
       tc_fence_after();
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -470,23 +481,23 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
       constexpr uint32_t id_o = umma_idesc_f16(0, 128, D) | kUmmaTransposeB;
       const uint32_t q0 = smem_u32(s_qt), kv0 = smem_u32(s_kv);
       const uint32_t lead = lane == 0;
+      const uint32_t dq = desc_lo_k(q0), dk = desc_lo_k(kv0), dv = desc_lo_mn(kv0 + Sh::kTile, kKpKeys * 128);
       auto scores = [&](int half, int st) {
-        const uint32_t a0 = q0 + half * Sh::kTile, b0 = kv0 + (st * 2) * Sh::kTile;
+        const uint32_t a0 = dq + half * (Sh::kTile >> 4), b0 = dk + st * (2 * Sh::kTile >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * (kKpKeys * 128) + (k & 3) * 32;
-          umma_f16_ss(s_addr + half * 128, umma_desc_sw128(a0 + off), umma_desc_sw128(b0 + off), id_s, k != 0, lead);
+          const uint32_t off = ((k >> 2) * (kKpKeys * 128) + (k & 3) * 32) >> 4;
+          umma_f16_ss(s_addr + half * 128, a0 + off, b0 + off, id_s, k != 0, lead);
         }
       };
-      auto output = [&](int half, int st, bool first) {
-        const uint32_t b0 = kv0 + (st * 2 + 1) * Sh::kTile;
+      auto output = [&](int half, int st, int u, bool first) {  // of keys 64 u .. 64 u + 63
+        const uint32_t b0 = dv + st * (2 * Sh::kTile >> 4);
 #pragma unroll
-        for (int k = 0; k < kKpKeys / 16; ++k)
-          umma_f16_ts(o_addr + half * D, s_addr + half * 128 + 8 * k, umma_desc_mn_sw128(b0 + 2048 * k, kKpKeys * 128), id_o,
-                      !first || k != 0, lead);
+        for (int k = u * (kKpKeys / 32); k < (u + 1) * (kKpKeys / 32); ++k)
+          umma_f16_ts(o_addr + half * D, s_addr + half * 128 + 8 * k, b0 + (2048 * k >> 4), id_o, !first || k != 0, lead);
       };
       auto wait = [&](uint32_t bar, uint32_t par) {
-        const bool ok = mbar_wait(bar, par, p.status, abort, p.wait_ns);
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, par, p.status, abort, p.wait_ns));
         tc_fence_after();
         return ok;
       };
@@ -498,7 +509,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
         last_bar = bar, last_par = par, committed = true;
       };
       if (tiles > 0) {
-        ok = wait(p_full(0), 0) && wait(p_full(1), 0) && wait(k_full(0), 0);  // queries, first keys
+        ok = wait(p_full(0, 0), 0) && wait(p_full(1, 0), 0) && wait(k_full(0), 0);  // queries, first keys
         if (ok) {
           scores(0, 0);
           commit(s_full(0), 0);
@@ -509,12 +520,16 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
       }
       for (int j = 0; j < tiles && ok; ++j) {
         const int st = j & 1, nx = (j + 1) & 1;
-        for (int half = 0; half < 2 && ok; ++half) {
-          // phase j + 1 of the weights (phase 0 was the queries)
-          ok = wait(p_full(half), (j + 1) & 1) && (half || wait(v_full(st), (j >> 1) & 1));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          ok = wait(p_full(half, 0), (j + 1) & 1) && (half || wait(v_full(st), (j >> 1) & 1));
           if (!ok) break;
-          output(half, st, j == 0);
-          commit(pv_done(half), j & 1);
+          output(half, st, 0, j == 0);
+          commit(pv_done(half, 0), j & 1);
+          ok = wait(p_full(half, 1), j & 1);
+          if (!ok) break;
+          output(half, st, 1, false);
+          commit(pv_done(half, 1), j & 1);
           if (half) commit(v_empty(st), (j >> 1) & 1);
           if (j + 1 < tiles) {
             ok = half || wait(k_full(nx), ((j + 1) >> 1) & 1);

@@ -419,6 +419,23 @@ def test_nan_states_reach_the_rows_that_attend_to_them(q4, rows):
         assert torch.isnan(out[:rows, 1]).any(-1).all()
 
 
+@pytest.mark.parametrize("rows,length,at", [(5, 40, 37), (300, 300, 150), (200, 700, 600)])
+@pytest.mark.parametrize("name", ["k_state", "v_state"])
+def test_nan_states_spare_the_rows_in_front_of_them(q4, rows, length, at, name):
+    """A bad block meets zero weights in the rows that do not attend to its key: they keep their values."""
+    g = torch.Generator().manual_seed(rows)
+    c, table = fill_cache(q4, g, [length], 2, 128, 64, 64)
+    q = torch.randn(rows, 4, 128, generator=g).half().cuda()
+    args = (q, c, table.cuda(), torch.tensor([length], dtype=torch.int32, device="cuda"),
+            torch.tensor([0, rows], dtype=torch.int32, device="cuda"))
+    want = q4.kv_attention(*args)
+    getattr(c, name)[int(table[0, at // 64]), 1, at % 64, 0, 0] = float("nan")
+    out = q4.kv_attention(*args)
+    before = at - (length - rows)  # rows in front of the key
+    assert torch.equal(out[:, :2], want[:, :2]) and torch.equal(out[:before], want[:before])
+    assert torch.isnan(out[before:, 2:]).any(-1).all()
+
+
 def test_an_attention_block_in_a_graph_and_on_streams(q4):
     """Projections in 8-bit integers, the cache, attention and a 4-bit output projection as they are used together:
     eagerly, captured once and replayed for later tokens, and two batches at once on two streams."""
