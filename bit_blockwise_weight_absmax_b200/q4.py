@@ -25,6 +25,7 @@ F16, BF16, F32 = 0, 1, 2
 QTYPES = {"nf4": NF4, "int4_sym": INT4_SYM, "int4_asym": INT4_ASYM}
 _DT = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 _DT_INV = {v: k for k, v in _DT.items()}
+_DT16 = (torch.float16, torch.bfloat16)
 DQ_GROUP = 256
 INT8_MAX_K = 131071  # Q4_INT8_MAX_K
 
@@ -507,7 +508,7 @@ def gemm(A: torch.Tensor, st: Q4State, out_dtype: torch.dtype | None = None, out
 def _elsewhere(t: torch.Tensor, stream):
     """None when t's device is current and no stream is given; otherwise the
     context that makes them current, under which the caller calls itself."""
-    if stream is None and t.is_cuda and t.device.index == torch.cuda.current_device():
+    if stream is None and t.is_cuda and t.get_device() == torch._C._cuda_getDevice():
         return None
     if not t.is_cuda:
         raise Q4Error("no CUDA device: libq4 has no CPU fallback" if not torch.cuda.is_available()
@@ -522,7 +523,7 @@ def _elsewhere(t: torch.Tensor, stream):
 def _current_stream(t: torch.Tensor) -> int:
     """The handle of the current stream of t's device (torch.cuda.current_stream
     builds an object for it, at 3 us a call)."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 WORKSPACE_HEAD = 16384  # Q4_WORKSPACE_HEAD: the part of a workspace that starts zero-filled
@@ -532,7 +533,7 @@ def _stream_workspace(device, stream: int, nbytes: int):
     """(pointer, bytes, owner) of the current stream's workspace."""
     if nbytes == 0:
         return None, 0, None
-    if torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_isCurrentStreamCapturing():
         t = torch.empty(nbytes, dtype=torch.uint8, device=device)
         t[:WORKSPACE_HEAD].zero_()
         return t.data_ptr(), nbytes, t
@@ -584,13 +585,17 @@ def int8_quantize_rows(X: torch.Tensor, stream=None) -> tuple:
 
 
 def _check_codes(name, codes, scale):
-    if codes.dtype != torch.int8 or codes.dim() != 2 or scale.dtype != torch.float32 or scale.dim() != 1:
+    """The row stride of int8 [rows, K] codes with float32 [rows] scales."""
+    cs, ss = codes.shape, scale.shape
+    if codes.dtype != torch.int8 or len(cs) != 2 or scale.dtype != torch.float32 or len(ss) != 1:
         raise Q4Error(f"{name} must be int8 [rows, K] codes with float32 [rows] scales")
-    if scale.shape[0] != codes.shape[0] or not scale.is_contiguous():
+    if ss[0] != cs[0] or not scale.is_contiguous():
         raise Q4Error(f"{name}: one contiguous scale per row is needed")
-    if codes.stride(1) != 1 or codes.stride(0) % 16 or codes.data_ptr() % 16:
+    ld, one = codes.stride()
+    if one != 1 or ld & 15 or codes.data_ptr() & 15:
         raise Q4Error(f"{name}: code rows must be adjacent bytes that begin at multiples of 16 bytes "
                       "(as int8_quantize_rows gives them)")
+    return ld
 
 
 def _check_bias_out(bias, out, M, N, out_dtype, dev):
@@ -704,43 +709,25 @@ class KVCache:
             if t.dtype != want or not t.is_contiguous() or t.device != c.device or \
                     t.shape != (c if want == torch.uint8 else st).shape:
                 raise Q4Error(f"{name} must be a contiguous {want} tensor like its partners")
-        s = _CKVCache()
-        s.head_dim, s.blocksize = self.head_dim, self.blocksize
-        s.kv_heads, s.page_size, s.pages = self.kv_heads, self.page_size, self.pages
-        s.k_codes, s.k_state = c.data_ptr(), st.data_ptr()
-        s.v_codes, s.v_state = self.v_codes.data_ptr(), self.v_state.data_ptr()
-        self._c = s
-        self._ref = ctypes.byref(s)
-        self._ws_need = {}  # (batch, rows, query heads) -> workspace bytes of attention
+        # asked for on every call, so plain attributes
+        put = lambda name, value: object.__setattr__(self, name, value)
+        put("device", c.device)
+        put("pages", c.shape[0])
+        put("kv_heads", c.shape[1])
+        put("page_size", c.shape[2])
+        put("head_dim", 2 * c.shape[3])
+        put("blocksize", self.head_dim // st.shape[3])
+        s = _CKVCache(self.head_dim, self.blocksize, self.kv_heads, self.page_size, self.pages, c.data_ptr(),
+                      st.data_ptr(), self.v_codes.data_ptr(), self.v_state.data_ptr())
+        put("_c", s)
+        put("_ref", ctypes.byref(s))
+        put("_ws_need", {})  # (batch, rows, query heads) -> workspace bytes of attention
+        put("_fixed", True)
 
     def __setattr__(self, name, value):
-        if name in ("k_codes", "k_state", "v_codes", "v_state") and "_c" in self.__dict__:
+        if "_fixed" in self.__dict__:
             raise Q4Error("the buffers of a KVCache are fixed: make a new one")
         object.__setattr__(self, name, value)
-
-    @property
-    def pages(self) -> int:
-        return self.k_codes.shape[0]
-
-    @property
-    def kv_heads(self) -> int:
-        return self.k_codes.shape[1]
-
-    @property
-    def page_size(self) -> int:
-        return self.k_codes.shape[2]
-
-    @property
-    def head_dim(self) -> int:
-        return 2 * self.k_codes.shape[3]
-
-    @property
-    def blocksize(self) -> int:
-        return self.head_dim // self.k_state.shape[3]
-
-    @property
-    def device(self):
-        return self.k_codes.device
 
     def held_bytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in (self.k_codes, self.k_state, self.v_codes, self.v_state))
@@ -762,24 +749,26 @@ def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, bloc
     return KVCache(c[0], s[0], c[1], s[1])
 
 
-def _head_rows(x: torch.Tensor, heads, dim: int, name: str) -> torch.Tensor:
-    """x as [rows, heads, dim] with strides the kernels read (a copy if its own are not)."""
-    _rows16(x, name)
-    if x.dim() != 3 or x.shape[2] != dim or (heads is not None and x.shape[1] != heads):
-        raise Q4Error(f"{name} must be [rows, {heads or 'heads'}, {dim}], got {tuple(x.shape)}")
-    if x.stride(2) != 1 or x.stride(0) % 8 or x.stride(1) % 8 or x.data_ptr() % 16 or x.stride(0) < 0:
+def _head_rows(x: torch.Tensor, heads, dim: int, name: str):
+    """x as [rows, heads, dim] with strides the kernels read (a copy if its own
+    are not), its shape, its token and head strides."""
+    shape, st = x.shape, x.stride()
+    if x.dtype not in _DT16 or len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise Q4Error(f"{name} must be float16 or bfloat16 [rows, {heads or 'heads'}, {dim}], got {x.dtype} "
+                      f"{tuple(shape)}")
+    if st[2] != 1 or st[0] & 7 or st[1] & 7 or st[0] < 0 or x.data_ptr() & 15:
         x = x.contiguous()
-        if x.data_ptr() % 16:
+        if x.data_ptr() & 15:
             x = x.clone()
-    return x
+        st = x.stride()
+    return x, shape, st[0], st[1]
 
 
-def _index(t: torch.Tensor, dtype, shape, name: str) -> torch.Tensor:
-    if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and t.shape[i] != w for i, w in enumerate(shape)):
-        raise Q4Error(f"{name} must be {dtype} of shape {shape}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_contiguous():
-        t = t.contiguous()
-    return t
+def _index(t: torch.Tensor, dtype, n: int | None, name: str) -> torch.Tensor:
+    """t as a contiguous 1-D tensor of n integers of dtype."""
+    if t.dtype != dtype or t.dim() != 1 or (n is not None and t.shape[0] != n):
+        raise Q4Error(f"{name} must be {dtype} of {'' if n is None else n} elements, got {t.dtype} {tuple(t.shape)}")
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
@@ -790,15 +779,16 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     if ctx is not None:
         with ctx:
             return kv_append(cache, k, v, slots)
-    k = _head_rows(k, cache.kv_heads, cache.head_dim, "k")
-    v = _head_rows(v, cache.kv_heads, cache.head_dim, "v")
-    if k.shape != v.shape or k.dtype != v.dtype:
+    k, shape, kt, kh = _head_rows(k, cache.kv_heads, cache.head_dim, "k")
+    v, v_shape, vt, vh = _head_rows(v, cache.kv_heads, cache.head_dim, "v")
+    if shape != v_shape or k.dtype != v.dtype:
         raise Q4Error("k and v must have one shape and dtype")
-    n = k.shape[0]
-    slots = _index(slots, torch.int64, (n,), "slots")
-    _same_device(k.device, v=v, slots=slots, cache=cache)
+    n = shape[0]
+    slots = _index(slots, torch.int64, n, "slots")
+    dev = k.device
+    if v.device != dev or slots.device != dev or cache.device != dev:
+        _same_device(dev, v=v, slots=slots, cache=cache)
     if n:
-        (kt, kh, _), (vt, vh, _) = k.stride(), v.stride()
         _check(library().q4_kv_append(cache._ref, k.data_ptr(), v.data_ptr(), _DT[k.dtype], n, kt, kh, vt, vh,
                                       slots.data_ptr(), _current_stream(k)), "q4_kv_append")
 
@@ -812,11 +802,10 @@ def kv_dequantize(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torc
     if ctx is not None:
         with ctx:
             return kv_dequantize(cache, slots, dtype)
-    slots = _index(slots, torch.int64, (None,), "slots")
+    slots = _index(slots, torch.int64, None, "slots")
     _same_device(slots.device, cache=cache)
     n = slots.shape[0]
-    k = torch.empty(n, cache.kv_heads, cache.head_dim, dtype=dtype, device=slots.device)
-    v = torch.empty_like(k)
+    k, v = torch.empty(2, n, cache.kv_heads, cache.head_dim, dtype=dtype, device=slots.device).unbind()
     if n:
         _check(library().q4_kv_dequantize(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _DT[dtype],
                                           _current_stream(slots)), "q4_kv_dequantize")
@@ -847,31 +836,36 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq
         with ctx:
             return kv_attention(q, cache, block_table, seq_lens, cu_seqlens_q, max_q, scale, causal, window, out, return_lse)
     dim = cache.head_dim
-    q = _head_rows(q, None, dim, "q")
-    rows, heads, _ = q.shape
+    q, shape, qt, qh = _head_rows(q, None, dim, "q")
+    rows, heads, _ = shape
     if heads == 0 or heads % cache.kv_heads:
         raise Q4Error(f"{heads} query heads are no multiple of {cache.kv_heads} key/value heads")
     if window < 0:
         raise Q4Error("window must be 0 (none) or positive")
-    seq_lens = _index(seq_lens, torch.int32, (None,), "seq_lens")
+    seq_lens = _index(seq_lens, torch.int32, None, "seq_lens")
     batch = seq_lens.shape[0]
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch or \
             block_table.shape[1] < 1:
         raise Q4Error(f"block_table must be int32 [{batch}, pages], got {block_table.dtype} "
                       f"{tuple(block_table.shape)}")
-    if block_table.stride(1) != 1 or block_table.stride(0) < block_table.shape[1]:
+    bt, one = block_table.stride()
+    pages = block_table.shape[1]
+    if one != 1 or bt < pages:
         block_table = block_table.contiguous()
+        bt = pages
     if cu_seqlens_q is not None:
-        cu_seqlens_q = _index(cu_seqlens_q, torch.int32, (batch + 1,), "cu_seqlens_q")
+        cu_seqlens_q = _index(cu_seqlens_q, torch.int32, batch + 1, "cu_seqlens_q")
     elif rows != batch:
         raise Q4Error(f"{rows} query rows for {batch} sequences: pass cu_seqlens_q")
-    _same_device(q.device, cache=cache, block_table=block_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q,
-                 out=out)
+    dev = q.device
+    if cache.device != dev or block_table.device != dev or seq_lens.device != dev or \
+            (cu_seqlens_q is not None and cu_seqlens_q.device != dev) or (out is not None and out.device != dev):
+        _same_device(dev, cache=cache, block_table=block_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q, out=out)
     if out is None:
-        out = torch.empty(rows, heads, dim, dtype=q.dtype, device=q.device)
+        out = torch.empty(rows, heads, dim, dtype=q.dtype, device=dev)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise Q4Error("out must be a contiguous tensor of q's shape and dtype")
-    lse = torch.empty(rows, heads, dtype=torch.float32, device=q.device) if return_lse else None
+    lse = torch.empty(rows, heads, dtype=torch.float32, device=dev) if return_lse else None
     if rows and batch:
         key = (batch, rows, heads)
         need = cache._ws_need.get(key)
@@ -883,13 +877,13 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq
                 cache._ws_need.clear()
             need = cache._ws_need[key] = n.value
         s = _current_stream(q)
-        ws, ws_bytes, _ = _stream_workspace(q.device, s, need)
+        ws, ws_bytes, _ = _stream_workspace(dev, s, need)
         if max_q is None:
             max_q = 1 if cu_seqlens_q is None else rows
         _check(library().q4_kv_attention(
-            cache._ref, q.data_ptr(), _DT[q.dtype], rows, heads, q.stride(0), q.stride(1),
+            cache._ref, q.data_ptr(), _DT[q.dtype], rows, heads, qt, qh,
             None if cu_seqlens_q is None else cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),
-            block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]), block_table.shape[1], batch,
+            block_table.data_ptr(), bt, pages, batch,
             max(1, max_q), 1.0 / math.sqrt(dim) if scale is None else scale, int(causal), window, out.data_ptr(),
             None if lse is None else lse.data_ptr(), ws, ws_bytes, s), "q4_kv_attention")
     return (out, lse) if return_lse else out
