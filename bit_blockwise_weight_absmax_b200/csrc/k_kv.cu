@@ -57,7 +57,7 @@ int go_prompt(const KvAttnParams &p, cudaStream_t st) {
   const int rc = set_smem_attr_once<kern>(KpShape<D>::kSmem, true);
   if (rc != Q4_OK) return rc;
   const int64_t rows = (int64_t)p.total_q * (p.q_heads / p.c.heads);
-  const int64_t tiles = (rows / kKpRows + std::min<int64_t>(p.batch, rows)) * p.c.heads;
+  const int64_t tiles = (rows / kKpRows + std::min<int64_t>(p.batch, rows)) * p.c.heads + p.sms;  // the last wave's parts
   if (tiles > INT32_MAX) return Q4_ERR_SHAPE;
   launch_pdl(kern, dim3((unsigned)tiles), dim3(kKpThreads), KpShape<D>::kSmem, st, p);
   return launched();
@@ -82,6 +82,8 @@ int run_kv_attention(int dt, int D, int B, const KvAttnParams &p, int64_t max_q,
   return by_format(dt, D, B, Attend{p, rows <= 8 ? 8 : rows <= 64 ? 16 : 256, sms, st});
 }
 size_t kv_attention_ws(int D, int sms) {
-  return kKvCountBytes + (size_t)2 * sms * 2 * 16 * (D + 2) * sizeof(float);
+  // few rows: two segments of 8 or 16 rows a CTA; many: a part of 256 rows an SM
+  const size_t few = (size_t)2 * sms * 2 * 16 * (D + 2), many = (size_t)sms * kKpRows * (D + 2);
+  return kKvCountBytes + std::max(few, many) * sizeof(float);
 }
 }  // namespace q4

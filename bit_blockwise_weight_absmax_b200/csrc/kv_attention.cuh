@@ -51,6 +51,7 @@ struct KvAttnParams {
   unsigned *counts;  // [CTA] arrivals at the segment that the CTA is the first of, zero between calls
   float *parts;      // [CTA][first or last segment][kPart] results of cut segments
   uint64_t wait_ns;
+  int32_t sms;
   int *status;
 };
 

@@ -22,6 +22,10 @@
 //                 O += P V (weights from tensor memory) for the two 128-row
 //                 halves in turn: while one half's softmax runs, the other's
 //                 products do.
+// Work: whole (256 rows, kv head) tiles in as many waves as there are; those of
+// the last, partly filled wave are cut along the keys over the idle SMs, their
+// partial outputs joined by the CTA that comes last (few rows over many keys
+// are all such tiles).
 // Tensor memory: two score tiles of 128 columns (weights over their first 64)
 // and two outputs of D.  Query rows are scaled by a power of two into binary16.
 #pragma once
@@ -32,6 +36,7 @@ namespace q4 {
 constexpr int kKpRows = 256;   // query rows of a CTA
 constexpr int kKpKeys = 128;   // keys of a tile
 constexpr int kKpThreads = 512;
+constexpr int kKpMinTiles = 4;         // key tiles a CTA takes of a tile that several share, at least
 constexpr float kKpAhead = 14.0f;    // scores up to this far past the reference keep it
 constexpr float kKpMost = 32768.0f;  // of a row's weights in a tile: each is inside binary16 then
 
@@ -127,7 +132,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
   uint8_t *s_kv = smem + 2 * Sh::kTile;  // [2 stages][keys, values][kTile]
   __shared__ uint64_t s_bar[18];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_where[4];
+  __shared__ int s_abort, s_where[4];  // [3]: this CTA joins the parts
   __shared__ int64_t s_scan[kKpThreads / 32];
   __shared__ uint4 s_bad[4];  // keys of a tile that no row may read
   // values that are the same in a warp are marked so (a shuffle): the MMA
@@ -185,7 +190,15 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
   if (lane == 31) s_scan[warp] = incl;
   __syncthreads();
   for (int w = 0; w < warp; ++w) incl += s_scan[w];
-  const int64_t x = blockIdx.x;
+  int64_t all = 0;
+  for (int w = 0; w < kKpThreads / 32; ++w) all += s_scan[w];
+  // the last wave's tiles: `share` CTAs each
+  const int64_t whole = all / p.sms * p.sms;
+  const int rest = (int)(all - whole), share = rest ? p.sms / rest : 1;
+  int64_t x = blockIdx.x;
+  const int part = x < whole ? 0 : (int)((x - whole) % share);
+  const int slot = (int)max((int64_t)0, x - whole) / share;  // which of the last wave's tiles
+  if (x >= whole) x = whole + (x - whole) / share;
   if (x >= incl - mine && x < incl) {
     int64_t at = incl - mine;
     int b = tid * per;
@@ -214,6 +227,16 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     hi_all = p.causal ? min(sq.len, p0 + i0 + 1) : sq.len;
     tile0 = lo_first / kKpKeys;
     tiles = max(0, (hi_last + kKpKeys - 1) / kKpKeys - tile0);
+  }
+  // this CTA's part of the keys
+  const int parts = (int)blockIdx.x < whole ? 1 : max(1, min(share, tiles / kKpMinTiles));
+  if (part >= parts) {
+    rows = 0;  // not needed: it ends like a CTA past the last tile
+    tiles = 0;
+  } else {
+    const int from = (int)((int64_t)tiles * part / parts);
+    tiles = (int)((int64_t)tiles * (part + 1) / parts) - from;
+    tile0 += from;
   }
   tiles = uniform(tiles);
   const uint32_t s_addr = tmem, o_addr = tmem + 256;
@@ -366,33 +389,99 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     }
     // ---- the row's output ----
     if (ok && tiles > 0) ok = mbar_wait_warp(pv_done(half, 1), (tiles - 1) & 1, p.status, abort, p.wait_ns);
-    if (ok && b >= 0) {
-      tc_fence_after();
+    tc_fence_after();
+    const int64_t at = (int64_t)(sq.q0 + i) * p.q_heads + h;
+    auto finish = [&](int c, const float (&o)[32], float inv) {  // columns 32 c .. of the row
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {  // word 4 c + v of the row
+        const int w = 4 * c + v;
+        uint4 out;
+        out.x = Dt<DT>::pack2(o[8 * v] * inv, o[8 * v + 2] * inv);
+        out.y = Dt<DT>::pack2(o[8 * v + 4] * inv, o[8 * v + 6] * inv);
+        out.z = Dt<DT>::pack2(o[8 * v + 1] * inv, o[8 * v + 3] * inv);
+        out.w = Dt<DT>::pack2(o[8 * v + 5] * inv, o[8 * v + 7] * inv);
+        *reinterpret_cast<uint4 *>(p.out + at * D + (w % NB) * B + 8 * (w / NB)) = out;
+      }
+    };
+    auto finish_lse = [&] {
+      if (p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m + __log2f(l)) * 0.69314718055994531f;
+    };
+    auto output = [&](int c, float (&o)[32]) {  // columns 32 c .. from tensor memory
+      uint32_t t[32];
+      if (tiles > 0) {
+        tmem_ld32(ot + 32 * c, t);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = tiles > 0 ? __uint_as_float(t[e]) : 0.0f;
+    };
+    if (ok && rows > 0 && parts == 1) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const int64_t at = (int64_t)(sq.q0 + i) * p.q_heads + h;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (tiles > 0) {
-          tmem_ld32(ot + 32 * c, o);
-          tmem_wait_ld();
-        }
-        if (!real) continue;
+        float o[32];
+        output(c, o);
+        if (l == 0.0f)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {  // word 4 c + v of the row
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = l == 0.0f ? 0.0f : __uint_as_float(o[8 * v + e]) * inv;
-          const int w = 4 * c + v;
-          uint4 out;
-          out.x = Dt<DT>::pack2(f[0], f[2]);
-          out.y = Dt<DT>::pack2(f[4], f[6]);
-          out.z = Dt<DT>::pack2(f[1], f[3]);
-          out.w = Dt<DT>::pack2(f[5], f[7]);
-          *reinterpret_cast<uint4 *>(p.out + at * D + (w % NB) * B + 8 * (w / NB)) = out;
-        }
+          for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+        if (real) finish(c, o, inv);
       }
-      if (real && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m + __log2f(l)) * 0.69314718055994531f;
+      if (real) finish_lse();
+    } else if (rows > 0 && parts > 1) {  // after a timeout too: all warps meet
+      // one of several parts: [part][D / 4][256 rows] float4, then (m, l)
+      constexpr int kPart = kKpRows * (D + 2);
+      float *base = p.parts + (int64_t)(slot * share) * kPart;
+      float4 *mine4 = reinterpret_cast<float4 *>(base + part * kPart) + r;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        output(c, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) __stcg(mine4 + (8 * c + e) * kKpRows, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+      }
+      __stcg(reinterpret_cast<float2 *>(base + part * kPart + kKpRows * D) + r, make_float2(m, l));
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (tid == 0) {
+        __threadfence();  // the part (ordered by the barrier) before its count
+        const unsigned old = atomicAdd(p.counts + slot, 1u);
+        s_where[3] = old == (unsigned)(parts - 1);
+        if (s_where[3]) p.counts[slot] = 0u;
+        __threadfence();
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (s_where[3]) {
+        m = -INFINITY;
+        for (int k = 0; k < parts; ++k)
+          m = fmaxf(m, __ldcg(reinterpret_cast<const float2 *>(base + k * kPart + kKpRows * D) + r).x);
+        l = 0.0f;
+        for (int k = 0; k < parts; ++k) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2 *>(base + k * kPart + kKpRows * D) + r);
+          l = fmaf(ml.y, ml.x == -INFINITY ? 0.0f : ex2(ml.x - m), l);
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+#pragma unroll 1
+          for (int k = 0; k < parts; ++k) {
+            const float mk = __ldcg(reinterpret_cast<const float2 *>(base + k * kPart + kKpRows * D) + r).x;
+            const float f = mk == -INFINITY ? 0.0f : ex2(mk - m);
+            const float4 *src = reinterpret_cast<const float4 *>(base + k * kPart) + r;
+            float4 t[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = ldcg_v4(reinterpret_cast<const float *>(src + (8 * c + e) * kKpRows));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              o[4 * e] = fmaf(t[e].x, f, o[4 * e]), o[4 * e + 1] = fmaf(t[e].y, f, o[4 * e + 1]);
+              o[4 * e + 2] = fmaf(t[e].z, f, o[4 * e + 2]), o[4 * e + 3] = fmaf(t[e].w, f, o[4 * e + 3]);
+            }
+          }
+          if (real) finish(c, o, inv);
+        }
+        if (real) finish_lse();
+      }
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ dequantize

@@ -245,6 +245,7 @@ int q4_kv_attention(const q4_kv_cache *cache, const void *Q, int32_t dtype, int6
   p.counts = (unsigned *)workspace;
   p.parts = (float *)((char *)workspace + kKvCountBytes);
   p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  p.sms = di.sms;
   p.status = di.status;
   return run_kv_attention(dtype, cache->head_dim, cache->blocksize, p, max_q, di.sms, (cudaStream_t)stream);
 }
