@@ -18,23 +18,45 @@ int by_format(int dt, int D, int B, F &&f) {
 }
 int launched() { return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA; }
 
+// Few tokens: one a thread, so that they spread over the SMs; many: kKvItems.
+template <int D, int ITEMS> bool kv_grid(int64_t tokens, int heads, dim3 *grid) {
+  constexpr int per = kKvThreads / (D / 8) * ITEMS;
+  const int64_t groups = (tokens + per - 1) / per;
+  *grid = dim3((unsigned)groups, (unsigned)heads, 2);
+  return groups <= INT32_MAX;
+}
+bool kv_many(int64_t tokens, int heads, int D, int sms) {
+  return tokens * heads * 2 * (D / 8) >= (int64_t)sms * 2048 * kKvItems;  // the SMs' threads, kKvItems each
+}
 struct Append {
   const KvAppendParams &p;
+  int sms;
   cudaStream_t st;
   template <int DT, int D, int B> int operator()() const {
-    const int64_t blocks = (p.tokens * p.c.heads * (D / 8) + kKvThreads - 1) / kKvThreads;
-    if (blocks > INT32_MAX) return Q4_ERR_SHAPE;
-    launch_pdl(kv_append_kernel<DT, D, B>, dim3((unsigned)blocks, 2), dim3(kKvThreads), 0, st, p);
+    dim3 grid;
+    if (kv_many(p.tokens, p.c.heads, D, sms)) {
+      if (!kv_grid<D, kKvItems>(p.tokens, p.c.heads, &grid)) return Q4_ERR_SHAPE;
+      launch_pdl(kv_append_kernel<DT, D, B, kKvItems>, grid, dim3(kKvThreads), 0, st, p);
+    } else {
+      kv_grid<D, 1>(p.tokens, p.c.heads, &grid);
+      launch_pdl(kv_append_kernel<DT, D, B, 1>, grid, dim3(kKvThreads), 0, st, p);
+    }
     return launched();
   }
 };
 struct Dequant {
   const KvDequantParams &p;
+  int sms;
   cudaStream_t st;
   template <int DT, int D, int B> int operator()() const {
-    const int64_t blocks = (p.n * p.c.heads * (D / 8) + kKvThreads - 1) / kKvThreads;
-    if (blocks > INT32_MAX) return Q4_ERR_SHAPE;
-    launch_pdl(kv_dequantize_kernel<DT, D, B>, dim3((unsigned)blocks, 2), dim3(kKvThreads), 0, st, p);
+    dim3 grid;
+    if (kv_many(p.n, p.c.heads, D, sms)) {
+      if (!kv_grid<D, kKvItems>(p.n, p.c.heads, &grid)) return Q4_ERR_SHAPE;
+      launch_pdl(kv_dequantize_kernel<DT, D, B, kKvItems>, grid, dim3(kKvThreads), 0, st, p);
+    } else {
+      kv_grid<D, 1>(p.n, p.c.heads, &grid);
+      launch_pdl(kv_dequantize_kernel<DT, D, B, 1>, grid, dim3(kKvThreads), 0, st, p);
+    }
     return launched();
   }
 };
@@ -62,6 +84,11 @@ int go_prompt(const KvAttnParams &p, cudaStream_t st) {
   launch_pdl(kern, dim3((unsigned)tiles), dim3(kKpThreads), KpShape<D>::kSmem, st, p);
   return launched();
 }
+// The most rows of a kv head that take the kernel for few rows.  Measured (us,
+// 8 kv heads, D = 128), few-rows kernel against the prompt kernel: 32 rows over
+// 16384 keys 28 / 63, 32 sequences of 4096 keys 109 / 139; 64 rows 43 / 64 and
+// 194 / 143.
+constexpr int64_t kFewRows = 48;
 struct Attend {
   const KvAttnParams &p;
   int rows, sms;
@@ -73,13 +100,15 @@ struct Attend {
 };
 }  // namespace
 
-int run_kv_append(int dt, int D, int B, const KvAppendParams &p, cudaStream_t st) { return by_format(dt, D, B, Append{p, st}); }
-int run_kv_dequantize(int dt, int D, int B, const KvDequantParams &p, cudaStream_t st) {
-  return by_format(dt, D, B, Dequant{p, st});
+int run_kv_append(int dt, int D, int B, const KvAppendParams &p, int sms, cudaStream_t st) {
+  return by_format(dt, D, B, Append{p, sms, st});
+}
+int run_kv_dequantize(int dt, int D, int B, const KvDequantParams &p, int sms, cudaStream_t st) {
+  return by_format(dt, D, B, Dequant{p, sms, st});
 }
 int run_kv_attention(int dt, int D, int B, const KvAttnParams &p, int64_t max_q, int sms, cudaStream_t st) {
   const int64_t rows = max_q * (p.q_heads / p.c.heads);
-  return by_format(dt, D, B, Attend{p, rows <= 8 ? 8 : rows <= 64 ? 16 : 256, sms, st});
+  return by_format(dt, D, B, Attend{p, rows <= 8 ? 8 : rows <= kFewRows ? 16 : 256, sms, st});
 }
 size_t kv_attention_ws(int D, int sms) {
   // few rows: two segments of 8 or 16 rows a CTA; many: a part of 256 rows an SM

@@ -9,9 +9,9 @@
 // Both kernels are bound by memory: 4 D bytes of K and V and D + 8 D / B bytes
 // of cache per token and head.  A thread owns 8 elements = one 16-byte load
 // and one word of codes; B / 8 lanes hold a block and find its range by
-// shuffles.  Items run over tokens fastest, so that a CTA writes adjacent
-// tokens of one head: with slots in order its codes and states are
-// contiguous runs of the page.
+// shuffles.  A CTA takes adjacent tokens of one head: with slots in order its
+// codes and states are contiguous runs of the page.  Calls of many tokens give
+// a thread kKvItems of them, whose loads are on their way together.
 #pragma once
 #include "q4_common.cuh"
 
@@ -40,71 +40,111 @@ struct KvAppendParams {
 };
 
 constexpr int kKvThreads = 256;
+constexpr int kKvItems = 4;
 constexpr float kKvMaxRange = 61440.0f;  // 15 * 4096: s (q - z) stays within binary16
 
-template <int DT, int D, int B>
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// grid: (token groups, heads, K or V)
+template <int DT, int D, int B, int ITEMS>
 __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
   pdl_launch_then_wait();
   constexpr int TV = D / 8;  // threads per vector
   constexpr int LB = B / 8;  // lanes per block
-  constexpr int NB = D / B;
-  const int which = blockIdx.y;
-  const int64_t item = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) / TV;
+  constexpr int NB = D / B, TPB = kKvThreads / TV;
+  const int which = blockIdx.z, head = blockIdx.y;
   const int w = threadIdx.x % TV;  // elements 8 w .. 8 w + 7
-  const int64_t n_items = p.tokens * p.c.heads;
-  int64_t slot = -1;
-  int head = 0;
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (item < n_items) {
-    head = (int)(item / p.tokens);
-    const int64_t token = item - (int64_t)head * p.tokens;
-    slot = __ldg(p.slots + token);
-    if (slot >= p.c.slots) {
+  const int64_t token0 = (int64_t)blockIdx.x * (TPB * ITEMS) + threadIdx.x / TV;
+  const uint16_t *x = p.x[which] + head * p.hs[which] + 8 * w;
+  int64_t slot[ITEMS];
+  uint4 v[ITEMS];
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int64_t token = token0 + k * TPB;
+    slot[k] = token < p.tokens ? __ldg(p.slots + token) : -1;
+    v[k] = token < p.tokens ? ldg_stream_v4(x + token * p.ts[which]) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[2 * j] = lo16<DT>(u[j]), f[2 * j + 1] = hi16<DT>(u[j]);
+    float mn = 0.0f, mx = 0.0f;  // NaN where an element is
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mn = min_nan(mn, f[j]), mx = max_nan(mx, f[j]);
+#pragma unroll
+    for (int o = LB / 2; o >= 1; o >>= 1) {
+      mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    }
+    if (slot[k] < 0) continue;
+    if (slot[k] >= p.c.slots) {
       if (w == 0) raise_status(p.status, Q4_STATUS_INDEX);
-      slot = -1;
+      continue;
     }
-    if (slot >= 0) v = ldg_stream_v4(p.x[which] + token * p.ts[which] + head * p.hs[which] + 8 * w);
-  }
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-  float f[8];
+    const float range = __fsub_rn(mx, mn);
+    const bool bad = !(range <= kKvMaxRange);
+    const float s = __half2float(__float2half_rn(__fdiv_rn(range, 15.0f)));
+    uint32_t word = 0;
+    float z = 0.0f;
+    if (!bad && s != 0.0f) {  // a binary16 s is at least 2^-24: inside div_markstein's range
+      const float y = __frcp_rn(s);
+      z = fminf(fmaxf(rintf(div_markstein(-mn, s, y)), 0.0f), 15.0f);
+      // rint(x / s) + z stands in the low bits of a sum with 1.5 * 2^23 (|x / s|
+      // is a few times 15 at most), clamped there to z's range
+      const uint64_t yy = f2_pack(y, y), ns = f2_pack(-s, -s), zz = f2_pack(z, z);
+      const uint64_t kr = f2_pack(12582912.0f, 12582912.0f);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) f[2 * j] = lo16<DT>(u[j]), f[2 * j + 1] = hi16<DT>(u[j]);
-  float mn = 0.0f, mx = 0.0f, sum = 0.0f;  // sum: NaN or infinite when an element is
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    mn = fminf(mn, f[j]);
-    mx = fmaxf(mx, f[j]);
-    sum += f[j] * 0.0f;
-  }
-#pragma unroll
-  for (int o = LB / 2; o >= 1; o >>= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
-  if (slot < 0) return;
-  const float range = __fsub_rn(mx, mn);
-  const bool bad = !(sum == 0.0f) || !(range <= kKvMaxRange);
-  const float s = __half2float(__float2half_rn(__fdiv_rn(range, 15.0f)));
-  uint32_t word = 0;
-  float z = 0.0f;
-  if (!bad && s != 0.0f) {  // a binary16 s is at least 2^-24: inside div_markstein's range
-    const float y = __frcp_rn(s);
-    z = fminf(fmaxf(rintf(div_markstein(-mn, s, y)), 0.0f), 15.0f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float q = fminf(fmaxf(rintf(div_markstein(f[j], s, y)) + z, 0.0f), 15.0f);
-      word |= (uint32_t)q << (4 * j);
+      for (int j = 3; j >= 0; --j) {
+        float r0, r1;
+        f2_unpack(f2_add(f2_add(div_markstein2(f2_pack(f[2 * j], f[2 * j + 1]), ns, yy), kr), zz), r0, r1);
+        r0 = fminf(fmaxf(r0, 12582912.0f), 12582927.0f);
+        r1 = fminf(fmaxf(r1, 12582912.0f), 12582927.0f);
+        word = (word << 8) | ((__float_as_uint(r1) & 15u) << 4) | (__float_as_uint(r0) & 15u);
+      }
+    }
+    const int64_t vec = kv_vec(p.c, slot[k], head);
+    const int blk = w / LB, i = w % LB;
+    reinterpret_cast<uint32_t *>(p.c.codes[which])[vec * TV + i * NB + blk] = word;
+    if (i == 0) {
+      const uint32_t sb = bad ? 0x7FFFu : (uint32_t)__half_as_ushort(__float2half_rn(s));
+      p.c.state[which][vec * NB + blk] = sb | ((uint32_t)__half_as_ushort(__float2half_rn(z)) << 16);
+      if (bad) raise_status(p.status, Q4_STATUS_NONFINITE);
     }
   }
-  const int64_t vec = kv_vec(p.c, slot, head);
-  const int blk = w / LB, i = w % LB;
-  reinterpret_cast<uint32_t *>(p.c.codes[which])[vec * TV + i * NB + blk] = word;
-  if (i == 0) {
-    const uint32_t sb = bad ? 0x7FFFu : (uint32_t)__half_as_ushort(__float2half_rn(s));
-    p.c.state[which][vec * NB + blk] = sb | ((uint32_t)__half_as_ushort(__float2half_rn(z)) << 16);
-    if (bad) raise_status(p.status, Q4_STATUS_NONFINITE);
-  }
+}
+
+// Eight codes of a word as binary16 s (code - z), pairs in the order of the
+// nibbles 04 15 26 37: 1024 + code is one masked OR, the difference exact, the
+// product rounded once.  z64 = -(64 + z), z1024 = -(1024 + z), both pairs.
+__device__ __forceinline__ uint4 kv_word(uint32_t w, __half2 s, __half2 z64, __half2 z1024) {
+  const __half2 sixteenth = __half2half2(__ushort_as_half(0x2C00));  // 1 / 16
+  auto h2 = [](uint32_t v) { return *reinterpret_cast<__half2 *>(&v); };
+  auto u2 = [](__half2 v) { return *reinterpret_cast<uint32_t *>(&v); };
+  const uint32_t w8 = w >> 8;
+  uint4 r;
+  r.x = u2(__hmul2(__hadd2(h2((w & 0x000F000Fu) | 0x64006400u), z1024), s));
+  r.y = u2(__hmul2(__hfma2(h2((w & 0x00F000F0u) | 0x64006400u), sixteenth, z64), s));
+  r.z = u2(__hmul2(__hadd2(h2((w8 & 0x000F000Fu) | 0x64006400u), z1024), s));
+  r.w = u2(__hmul2(__hfma2(h2((w8 & 0x00F000F0u) | 0x64006400u), sixteenth, z64), s));
+  return r;
+}
+// -(64 + z) and -(1024 + z) of a state's word, in pairs.
+__device__ __forceinline__ __half2 kv_z64(__half2 state) {
+  return __hsub2(__half2half2(__ushort_as_half(0xD400)), __high2half2(state));
+}
+__device__ __forceinline__ __half2 kv_z1024(__half2 state) {
+  return __hsub2(__half2half2(__ushort_as_half(0xE400)), __high2half2(state));
 }
 
 struct KvDequantParams {
@@ -115,34 +155,49 @@ struct KvDequantParams {
   int *status;
 };
 
-template <int DT, int D, int B>
+template <int DT, int D, int B, int ITEMS>
 __global__ void __launch_bounds__(kKvThreads) kv_dequantize_kernel(const __grid_constant__ KvDequantParams p) {
   pdl_launch_then_wait();
-  constexpr int TV = D / 8, LB = B / 8, NB = D / B;
-  const int which = blockIdx.y;
-  const int64_t item = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) / TV;
-  const int w = threadIdx.x % TV;
-  if (item >= p.n * p.c.heads) return;
-  const int head = (int)(item / p.n);
-  const int64_t row = item - (int64_t)head * p.n;
-  const int64_t slot = __ldg(p.slots + row);
-  uint4 o = make_uint4(0, 0, 0, 0);
-  if (slot >= p.c.slots) {
-    if (w == 0) raise_status(p.status, Q4_STATUS_INDEX);
-  } else if (slot >= 0) {
-    const int64_t vec = kv_vec(p.c, slot, head);
-    const int blk = w / LB, i = w % LB;
-    const uint32_t word = __ldg(reinterpret_cast<const uint32_t *>(p.c.codes[which]) + vec * TV + i * NB + blk);
-    const uint32_t st = __ldg(p.c.state[which] + vec * NB + blk);
-    const float s = __half2float(__ushort_as_half((unsigned short)(st & 0xFFFFu)));
-    const float z = __half2float(__ushort_as_half((unsigned short)(st >> 16)));
-    uint32_t r[4];
+  constexpr int TV = D / 8, LB = B / 8, NB = D / B, TPB = kKvThreads / TV;
+  const int which = blockIdx.z, head = blockIdx.y;
+  const int w = threadIdx.x % TV, blk = w / LB, i = w % LB;
+  const int64_t row0 = (int64_t)blockIdx.x * (TPB * ITEMS) + threadIdx.x / TV;
+  uint32_t word[ITEMS], st[ITEMS];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      r[j] = Dt<DT>::pack2(s * ((float)((word >> (8 * j)) & 15u) - z), s * ((float)((word >> (8 * j + 4)) & 15u) - z));
-    o = make_uint4(r[0], r[1], r[2], r[3]);
+  for (int k = 0; k < ITEMS; ++k) {
+    const int64_t row = row0 + k * TPB;
+    const int64_t slot = row < p.n ? __ldg(p.slots + row) : -1;
+    word[k] = st[k] = 0;  // zeros
+    if (slot >= p.c.slots) {
+      if (w == 0) raise_status(p.status, Q4_STATUS_INDEX);
+    } else if (slot >= 0) {
+      const int64_t vec = kv_vec(p.c, slot, head);
+      word[k] = __ldg(reinterpret_cast<const uint32_t *>(p.c.codes[which]) + vec * TV + i * NB + blk);
+      st[k] = __ldg(p.c.state[which] + vec * NB + blk);
+    }
   }
-  *reinterpret_cast<uint4 *>(p.x[which] + (row * p.c.heads + head) * D + 8 * w) = o;
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const int64_t row = row0 + k * TPB;
+    if (row >= p.n) break;
+    const __half2 sz = *reinterpret_cast<const __half2 *>(&st[k]);
+    // binary16: the products themselves; bf16: the exact differences, times s
+    // in binary32
+    const __half2 s = DT == Q4_F16 ? __low2half2(sz) : __half2half2(__ushort_as_half(0x3C00));
+    uint4 r = kv_word(word[k], s, kv_z64(sz), kv_z1024(sz));  // pairs 04 15 26 37
+    uint4 o;
+    if constexpr (DT == Q4_F16) {
+      o.x = __byte_perm(r.x, r.y, 0x5410), o.y = __byte_perm(r.z, r.w, 0x5410);
+      o.z = __byte_perm(r.x, r.y, 0x7632), o.w = __byte_perm(r.z, r.w, 0x7632);
+    } else {
+      const float sf = __low2float(sz);
+      auto f2 = [](uint32_t v) { return __half22float2(*reinterpret_cast<__half2 *>(&v)); };
+      const float2 a = f2(r.x), b = f2(r.y), c = f2(r.z), d = f2(r.w);
+      o.x = Dt<DT>::pack2(sf * a.x, sf * b.x), o.y = Dt<DT>::pack2(sf * c.x, sf * d.x);
+      o.z = Dt<DT>::pack2(sf * a.y, sf * b.y), o.w = Dt<DT>::pack2(sf * c.y, sf * d.y);
+    }
+    *reinterpret_cast<uint4 *>(p.x[which] + (row * p.c.heads + head) * D + 8 * w) = o;
+  }
 }
 
 }  // namespace q4

@@ -106,21 +106,6 @@ constexpr uint32_t kUmmaTransposeB = 1u << 16;
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// Eight codes of a word as binary16 s (code - z), pairs in the order of the
-// nibbles 04 15 26 37.  z64 = -(64 + z), z1024 = -(1024 + z), both pairs.
-__device__ __forceinline__ uint4 kv_word(uint32_t w, __half2 s, __half2 z64, __half2 z1024) {
-  const __half2 sixteenth = __half2half2(__ushort_as_half(0x2C00));  // 1 / 16
-  auto h2 = [](uint32_t v) { return *reinterpret_cast<__half2 *>(&v); };
-  auto u2 = [](__half2 v) { return *reinterpret_cast<uint32_t *>(&v); };
-  const uint32_t w8 = w >> 8;
-  uint4 r;
-  r.x = u2(__hmul2(__hadd2(h2((w & 0x000F000Fu) | 0x64006400u), z1024), s));
-  r.y = u2(__hmul2(__hfma2(h2((w & 0x00F000F0u) | 0x64006400u), sixteenth, z64), s));
-  r.z = u2(__hmul2(__hadd2(h2((w8 & 0x000F000Fu) | 0x64006400u), z1024), s));
-  r.w = u2(__hmul2(__hfma2(h2((w8 & 0x00F000F0u) | 0x64006400u), sixteenth, z64), s));
-  return r;
-}
-
 template <int DT, int D, int B>
 __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_constant__ KvAttnParams p) {
   using Sh = KpShape<D>;
@@ -525,9 +510,8 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
         const __half2 sz = *reinterpret_cast<const __half2 *>(&state[which][n]);
         s[n] = __low2half2(sz);
         if (poison) s[n] = __half2half2(__ushort_as_half(which == 0 ? 0x7FFF : 0));
-        const __half2 z = __high2half2(sz);
-        z64[n] = __hsub2(__half2half2(__ushort_as_half(0xD400)), z);    // -64 - z
-        z1024[n] = __hsub2(__half2half2(__ushort_as_half(0xE400)), z);  // -1024 - z
+        z64[n] = kv_z64(sz);
+        z1024[n] = kv_z1024(sz);
       }
 #pragma unroll
       for (int v = 0; v < V4; ++v) {

@@ -181,7 +181,7 @@ int q4_kv_append(const q4_kv_cache *cache, const void *K, const void *V, int32_t
   p.slots = slots;
   p.tokens = tokens;
   p.status = di.status;
-  return run_kv_append(dtype, cache->head_dim, cache->blocksize, p, (cudaStream_t)stream);
+  return run_kv_append(dtype, cache->head_dim, cache->blocksize, p, di.sms, (cudaStream_t)stream);
 }
 
 int q4_kv_dequantize(const q4_kv_cache *cache, const int64_t *slots, int64_t n, void *K, void *V, int32_t dtype,
@@ -198,7 +198,7 @@ int q4_kv_dequantize(const q4_kv_cache *cache, const int64_t *slots, int64_t n, 
   p.slots = slots;
   p.n = n;
   p.status = di.status;
-  return run_kv_dequantize(dtype, cache->head_dim, cache->blocksize, p, (cudaStream_t)stream);
+  return run_kv_dequantize(dtype, cache->head_dim, cache->blocksize, p, di.sms, (cudaStream_t)stream);
 }
 
 int q4_kv_attention_workspace_size(const q4_kv_cache *cache, int64_t batch, int64_t total_q, int32_t q_heads,

@@ -27,8 +27,8 @@ int run_int8_quantize(int dt, const I8QuantParams &p, cudaStream_t st);
 bool int8_gemv_ok(int64_t M, int64_t K);
 int run_int8_gemv(int x_dtype, const I8GemvParams &p, int sms, cudaStream_t st);
 int run_int8_gemm(const I8Operands &o, const I8Plan &pl, I8GemmParams &p, cudaStream_t st);
-int run_kv_append(int dt, int D, int B, const KvAppendParams &p, cudaStream_t st);
-int run_kv_dequantize(int dt, int D, int B, const KvDequantParams &p, cudaStream_t st);
+int run_kv_append(int dt, int D, int B, const KvAppendParams &p, int sms, cudaStream_t st);
+int run_kv_dequantize(int dt, int D, int B, const KvDequantParams &p, int sms, cudaStream_t st);
 int run_kv_attention(int dt, int D, int B, const KvAttnParams &p, int64_t max_q, int sms, cudaStream_t st);
 // Workspace of the attention on a device of `sms` SMs.
 size_t kv_attention_ws(int D, int sms);
