@@ -139,6 +139,14 @@ __device__ __forceinline__ uint4 kv_word(uint32_t w, __half2 s, __half2 z64, __h
   r.w = u2(__hmul2(__hfma2(h2((w8 & 0x00F000F0u) | 0x64006400u), sixteenth, z64), s));
   return r;
 }
+// s d - r for the differences d and their rounded products r: exact.
+__device__ __forceinline__ uint4 kv_rest(uint4 d, __half2 s, uint4 r) {
+  auto rest = [&](uint32_t a, uint32_t b) {
+    const __half2 v = __hfma2(*reinterpret_cast<__half2 *>(&a), s, __hneg2(*reinterpret_cast<__half2 *>(&b)));
+    return *reinterpret_cast<const uint32_t *>(&v);
+  };
+  return make_uint4(rest(d.x, r.x), rest(d.y, r.y), rest(d.z, r.z), rest(d.w, r.w));
+}
 // -(64 + z) and -(1024 + z) of a state's word, in pairs.
 __device__ __forceinline__ __half2 kv_z64(__half2 state) {
   return __hsub2(__half2half2(__ushort_as_half(0xD400)), __high2half2(state));

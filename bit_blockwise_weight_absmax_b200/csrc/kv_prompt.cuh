@@ -29,6 +29,8 @@
 // Tensor memory: two score tiles of 128 columns (weights over their first 64)
 // and two outputs of D.  Query rows are scaled by a power of two into binary16.
 #pragma once
+#include <type_traits>
+
 #include "kv_attention.cuh"
 
 namespace q4 {
@@ -37,13 +39,14 @@ constexpr int kKpRows = 256;   // query rows of a CTA
 constexpr int kKpKeys = 128;   // keys of a tile
 constexpr int kKpThreads = 512;
 constexpr int kKpMinTiles = 4;         // key tiles a CTA takes of a tile that several share, at least
+constexpr int kKpExact = 16;           // CTAs of up to this many key tiles multiply the keys unrounded
 constexpr float kKpAhead = 14.0f;    // scores up to this far past the reference keep it
 constexpr float kKpMost = 32768.0f;  // of a row's weights in a tile: each is inside binary16 then
 
 template <int D> struct KpShape {
   static constexpr int kHalves = D / 64;                       // 128-byte wide parts of a row
   static constexpr int kTile = kHalves * kKpKeys * 128;        // a key or value tile, also 128 query rows
-  static constexpr int kSmem = 2 * kTile + 4 * kTile + 1024;   // queries, two stages of keys and values
+  static constexpr int kSmem = 2 * kTile + 4 * kTile + kTile + 1024;  // queries, two stages of keys and values, key remainders
 };
 
 // 32 columns of this warp's 32 lanes of tensor memory, without waiting.
@@ -115,6 +118,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
   uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *s_qt = smem;                  // [2 halves of rows][kTile]
   uint8_t *s_kv = smem + 2 * Sh::kTile;  // [2 stages][keys, values][kTile]
+  uint8_t *s_lo = smem + 6 * Sh::kTile;  // what rounding the keys to binary16 left over (one stage)
   __shared__ uint64_t s_bar[18];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_where[4];  // [3]: this CTA joins the parts
@@ -213,6 +217,11 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     tile0 = lo_first / kKpKeys;
     tiles = max(0, (hi_last + kKpKeys - 1) / kKpKeys - tile0);
   }
+  // s (q - z) has up to 15 bits, binary16 holds 11: over many keys the
+  // roundings average out of a row's sum, over few they would show in it (log
+  // sum exp off by 2e-4 for a row of one key).  CTAs of few keys multiply the
+  // remainders too.
+  const bool exact = uniform(tiles) <= kKpExact;
   // this CTA's part of the keys
   const int parts = (int)blockIdx.x < whole ? 1 : max(1, min(share, tiles / kKpMinTiles));
   if (part >= parts) {
@@ -501,7 +510,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
 #pragma unroll
         for (int n = 0; n < NB; ++n) state[w][n] = there ? __ldg(p.c.state[w] + vec * NB + n) : 0u;
     };
-    auto store = [&](int which, int stage, bool poison) {
+    auto store = [&](auto remainder, int which, int stage, bool poison) {
       // the row's base with the swizzle's XOR in it: chunk c lies at base ^ 16 c
       const uint32_t dst = smem_u32(s_kv + (stage * 2 + which) * Sh::kTile + kk * 128) + ((kk & 7) << 4);
       __half2 s[NB], z64[NB], z1024[NB];
@@ -519,33 +528,45 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int w = 4 * v + e, n = w % NB;
-          st_shared_v4((dst ^ ((w & 7) << 4)) + (w >> 3) * (kKpKeys * 128), kv_word(w4[e], s[n], z64[n], z1024[n]));
+          const uint32_t at = (dst ^ ((w & 7) << 4)) + (w >> 3) * (kKpKeys * 128);
+          const uint4 r = kv_word(w4[e], s[n], z64[n], z1024[n]);
+          st_shared_v4(at, r);
+          if constexpr (decltype(remainder)::value) {
+            const uint4 d = kv_word(w4[e], __half2half2(__ushort_as_half(0x3C00)), z64[n], z1024[n]);  // code - z
+            st_shared_v4(at + smem_u32(s_lo) - smem_u32(s_kv + (stage * 2 + which) * Sh::kTile), kv_rest(d, s[n], r));
+          }
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
     };
-    load(0, page_of(0));
-    int pg_next = page_of(1);
-    for (int j = 0; j < tiles; ++j) {
-      const int st = j & 1;
-      // a value that is not finite must not meet the zero weights of rows that
-      // do not attend to it: it becomes zero, and its key NaN, so that the rows
-      // that do attend give NaN
-      bool poison = false;
+    auto tiles_in = [&](auto exact_tag) {
+      load(0, page_of(0));
+      int pg_next = page_of(1);
+      for (int j = 0; j < tiles; ++j) {
+        const int st = j & 1;
+        // a value that is not finite must not meet the zero weights of rows that
+        // do not attend to it: it becomes zero, and its key NaN, so that the rows
+        // that do attend give NaN
+        bool poison = false;
 #pragma unroll
-      for (int n = 0; n < NB; ++n) poison |= (state[1][n] & 0x7C00u) == 0x7C00u;
-      const uint32_t bad = __ballot_sync(0xffffffffu, bad_page);
-      if (lane == 0) reinterpret_cast<uint32_t *>(&s_bad[j & 3])[warp - 8] = bad;
-      if (!mbar_wait_warp(k_empty(st), ((j >> 1) & 1) ^ 1, p.status, abort, p.wait_ns)) break;
-      store(0, st, poison);
-      if (lane == 0) mbar_arrive(k_full(st));
-      if (!mbar_wait_warp(v_empty(st), ((j >> 1) & 1) ^ 1, p.status, abort, p.wait_ns)) break;
-      store(1, st, poison);
-      if (lane == 0) mbar_arrive(v_full(st));
-      if (j + 1 < tiles) load(j + 1, pg_next);
-      pg_next = page_of(j + 2);
-    }
+        for (int n = 0; n < NB; ++n) poison |= (state[1][n] & 0x7C00u) == 0x7C00u;
+        const uint32_t bad = __ballot_sync(0xffffffffu, bad_page);
+        if (lane == 0) reinterpret_cast<uint32_t *>(&s_bad[j & 3])[warp - 8] = bad;
+        if (!mbar_wait_warp(k_empty(st), ((j >> 1) & 1) ^ 1, p.status, abort, p.wait_ns)) break;
+        // the one stage of remainders: the tile before has been multiplied
+        if (decltype(exact_tag)::value && j > 0 && !mbar_wait_warp(k_empty(st ^ 1), ((j - 1) >> 1) & 1, p.status, abort, p.wait_ns)) break;
+        store(exact_tag, 0, st, poison);
+        if (lane == 0) mbar_arrive(k_full(st));
+        if (!mbar_wait_warp(v_empty(st), ((j >> 1) & 1) ^ 1, p.status, abort, p.wait_ns)) break;
+        store(std::false_type{}, 1, st, poison);
+        if (lane == 0) mbar_arrive(v_full(st));
+        if (j + 1 < tiles) load(j + 1, pg_next);
+        pg_next = page_of(j + 2);
+      }
+    };
+    if (exact) tiles_in(std::true_type{});
+    else tiles_in(std::false_type{});
   } else {
     
     if (warp == 12) {
@@ -554,13 +575,21 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
       constexpr uint32_t id_o = umma_idesc_f16(0, 128, D) | kUmmaTransposeB;
       const uint32_t q0 = smem_u32(s_qt), kv0 = smem_u32(s_kv);
       const uint32_t lead = lane == 0;
-      const uint32_t dq = desc_lo_k(q0), dk = desc_lo_k(kv0), dv = desc_lo_mn(kv0 + Sh::kTile, kKpKeys * 128);
-      auto scores = [&](int half, int st) {
+      const uint32_t dq = desc_lo_k(q0), dk = desc_lo_k(kv0), dv = desc_lo_mn(kv0 + Sh::kTile, kKpKeys * 128),
+                     dl = desc_lo_k(smem_u32(s_lo));
+      auto scores = [&](auto exact_tag, int half, int st) {
         const uint32_t a0 = dq + half * (Sh::kTile >> 4), b0 = dk + st * (2 * Sh::kTile >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = ((k >> 2) * (kKpKeys * 128) + (k & 3) * 32) >> 4;
           umma_f16_ss(s_addr + half * 128, a0 + off, b0 + off, id_s, k != 0, lead);
+        }
+        if constexpr (decltype(exact_tag)::value) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * (kKpKeys * 128) + (k & 3) * 32) >> 4;
+            umma_f16_ss(s_addr + half * 128, a0 + off, dl + off, id_s, true, lead);
+          }
         }
       };
       auto output = [&](int half, int st, int u, bool first) {  // of keys 64 u .. 64 u + 63
@@ -581,38 +610,43 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
         umma_commit_lead(bar, lead);
         last_bar = bar, last_par = par, committed = true;
       };
-      if (tiles > 0) {
-        ok = wait(p_full(0, 0), 0) && wait(p_full(1, 0), 0) && wait(k_full(0), 0);  // queries, first keys
-        if (ok) {
-          scores(0, 0);
-          commit(s_full(0), 0);
-          scores(1, 0);
-          commit(s_full(1), 0);
-          commit(k_empty(0), 0);
-        }
-      }
-      for (int j = 0; j < tiles && ok; ++j) {
-        const int st = j & 1, nx = (j + 1) & 1;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          ok = wait(p_full(half, 0), (j + 1) & 1) && (half || wait(v_full(st), (j >> 1) & 1));
-          if (!ok) break;
-          output(half, st, 0, j == 0);
-          commit(pv_done(half, 0), j & 1);
-          ok = wait(p_full(half, 1), j & 1);
-          if (!ok) break;
-          output(half, st, 1, false);
-          commit(pv_done(half, 1), j & 1);
-          if (half) commit(v_empty(st), (j >> 1) & 1);
-          if (j + 1 < tiles) {
-            ok = half || wait(k_full(nx), ((j + 1) >> 1) & 1);
-            if (!ok) break;
-            scores(half, nx);
-            commit(s_full(half), (j + 1) & 1);
-            if (half) commit(k_empty(nx), ((j + 1) >> 1) & 1);
+      // (two versions of the loop: one with a test inside took 6 % longer)
+      auto products = [&](auto exact_tag) {
+        if (tiles > 0) {
+          ok = wait(p_full(0, 0), 0) && wait(p_full(1, 0), 0) && wait(k_full(0), 0);  // queries, first keys
+          if (ok) {
+            scores(exact_tag, 0, 0);
+            commit(s_full(0), 0);
+            scores(exact_tag, 1, 0);
+            commit(s_full(1), 0);
+            commit(k_empty(0), 0);
           }
         }
-      }
+        for (int j = 0; j < tiles && ok; ++j) {
+          const int st = j & 1, nx = (j + 1) & 1;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            ok = wait(p_full(half, 0), (j + 1) & 1) && (half || wait(v_full(st), (j >> 1) & 1));
+            if (!ok) break;
+            output(half, st, 0, j == 0);
+            commit(pv_done(half, 0), j & 1);
+            ok = wait(p_full(half, 1), j & 1);
+            if (!ok) break;
+            output(half, st, 1, false);
+            commit(pv_done(half, 1), j & 1);
+            if (half) commit(v_empty(st), (j >> 1) & 1);
+            if (j + 1 < tiles) {
+              ok = half || wait(k_full(nx), ((j + 1) >> 1) & 1);
+              if (!ok) break;
+              scores(exact_tag, half, nx);
+              commit(s_full(half), (j + 1) & 1);
+              if (half) commit(k_empty(nx), ((j + 1) >> 1) & 1);
+            }
+          }
+        }
+      };
+      if (exact) products(std::true_type{});
+      else products(std::false_type{});
       // every MMA issued completes before TMEM is freed, also after a timeout
       if (committed) {
         int dummy = 0;
