@@ -52,6 +52,7 @@ struct KvAttnParams {
   float *parts;      // [CTA][first or last segment][kPart] results of cut segments
   uint64_t wait_ns;
   int32_t sms;
+  int32_t stall_copies;  // test hook: no keys and values are brought in
   int *status;
 };
 
@@ -554,6 +555,7 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   };
   uint32_t there = 0;  // bit stage * 2 + part: the part was copied
   auto issue = [&](int key, int pg, uint32_t no) {
+    if (p.stall_copies) return;
     const int st = no % Sh::kStages;
     const bool good = pg >= 0 && pg < pages;
     if (!good && pg != kNoPage) raise_status(p.status, Q4_STATUS_INDEX);

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_abort = 0;
-    s_where[0] = -1;
+    s_where[0] = -1, s_where[1] = s_where[2] = 0;  // no tile
   }
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512));
@@ -181,9 +181,14 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
   for (int w = 0; w < warp; ++w) incl += s_scan[w];
   int64_t all = 0;
   for (int w = 0; w < kKpThreads / 32; ++w) all += s_scan[w];
-  // the last wave's tiles: `share` CTAs each
+  // the last wave's tiles: `share` CTAs each, where the grid has room for them
+  // (row ranges that overlap make more tiles than it was sized for: those past
+  // it stay undone and are reported)
   const int64_t whole = all / p.sms * p.sms;
-  const int rest = (int)(all - whole), share = rest ? p.sms / rest : 1;
+  const int rest = (int)(all - whole);
+  int share = rest ? p.sms / rest : 1;
+  if (whole + (int64_t)rest * share > gridDim.x) share = 1;
+  if (all > gridDim.x && tid == 0) raise_status(p.status, Q4_STATUS_INDEX);
   int64_t x = blockIdx.x;
   const int part = x < whole ? 0 : (int)((x - whole) % share);
   const int slot = (int)max((int64_t)0, x - whole) / share;  // which of the last wave's tiles
@@ -479,7 +484,6 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ dequantize
-    
     const int kk = tid - 256;  // key of a tile
     const int pages = (int)(p.c.slots >> p.c.page_log2), page_mask = (1 << p.c.page_log2) - 1;
     const int32_t *table = b >= 0 ? p.table + (int64_t)b * p.table_stride : nullptr;
@@ -541,9 +545,9 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
       __syncwarp();
     };
     auto tiles_in = [&](auto exact_tag) {
-      load(0, page_of(0));
+      if (tiles > 0) load(0, page_of(0));
       int pg_next = page_of(1);
-      for (int j = 0; j < tiles; ++j) {
+      for (int j = 0; j < tiles && !p.stall_copies; ++j) {
         const int st = j & 1;
         // a value that is not finite must not meet the zero weights of rows that
         // do not attend to it: it becomes zero, and its key NaN, so that the rows
@@ -568,7 +572,6 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     if (exact) tiles_in(std::true_type{});
     else tiles_in(std::false_type{});
   } else {
-    
     if (warp == 12) {
       // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t id_s = umma_idesc_f16(0, 128, kKpKeys);

@@ -224,7 +224,7 @@ int q4_kv_attention(const q4_kv_cache *cache, const void *Q, int32_t dtype, int6
   size_t need = 0;
   rc = q4_kv_attention_workspace_size(cache, batch, total_q, q_heads, &need);
   if (rc != Q4_OK) return rc;
-  if ((!cu_q && total_q != batch) || max_q < 1 || window < 0 || table_pages < 1 || table_stride < table_pages ||
+  if ((!cu_q && total_q != batch) || max_q < 1 || window < 0 || table_pages < 1 || table_pages > INT32_MAX || table_stride < table_pages ||
       table_pages * cache->page_size > INT32_MAX - 65536 || q_token_stride < 0 || q_head_stride < 0)
     return Q4_ERR_SHAPE;
   if (!aligned16(Q) || !aligned16(out) || q_token_stride % 8 || q_head_stride % 8 || !aligned16(workspace)) return Q4_ERR_ALIGN;
@@ -246,6 +246,7 @@ int q4_kv_attention(const q4_kv_cache *cache, const void *Q, int32_t dtype, int6
   p.parts = (float *)((char *)workspace + kKvCountBytes);
   p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   p.sms = di.sms;
+  p.stall_copies = g_copy_stall.load(std::memory_order_relaxed);
   p.status = di.status;
   return run_kv_attention(dtype, cache->head_dim, cache->blocksize, p, max_q, di.sms, (cudaStream_t)stream);
 }

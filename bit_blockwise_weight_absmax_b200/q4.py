@@ -262,8 +262,9 @@ def set_wait_limit_ns(ns: int):
 
 
 def set_copy_stall(on: bool):
-    """Test hook: while on, the decode GEMV issues no weight copies, so its
-    stage waits run out after the wait limit (Q4_STATUS_TIMEOUT)."""
+    """Test hook: while on, the kernels with copy pipelines (GEMV, GEMM, grouped
+    quantize, int8 GEMM, cache attention) bring in no operands, so their stage
+    waits run out after the wait limit (Q4_STATUS_TIMEOUT)."""
     _check(library().q4_set_copy_stall(int(bool(on))), "q4_set_copy_stall")
 
 
@@ -592,7 +593,7 @@ def _check_codes(name, codes, scale):
     if ss[0] != cs[0] or not scale.is_contiguous():
         raise Q4Error(f"{name}: one contiguous scale per row is needed")
     ld, one = codes.stride()
-    if one != 1 or ld & 15 or codes.data_ptr() & 15:
+    if one != 1 or ld & 15 or ld < cs[1] or codes.data_ptr() & 15:
         raise Q4Error(f"{name}: code rows must be adjacent bytes that begin at multiples of 16 bytes "
                       "(as int8_quantize_rows gives them)")
     return ld
@@ -829,6 +830,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq
     own position; window > 0: only to the last `window` of them.  Rows that
     attend to nothing are zero, with log sum exp -inf; rows outside
     cu_seqlens_q are left as they were (pass `out` to have them defined).
+    At most 65535 sequences a call.
     Returns out [rows, q_heads, head_dim], with return_lse also float32 [rows,
     q_heads]."""
     ctx = _elsewhere(q, stream)

@@ -356,8 +356,9 @@ Q4_API int q4_int8_quantize_rows(const void *X, int32_t x_dtype, int64_t rows, i
 
 /*
  * q4_int8_gemm -- Y[M, N] = a_scale[m] w_scale[n] sum_k A[m, k] W[n, k] + bias[n]:
- * the sum in 32-bit integers (exact), then binary32 with one rounding to
- * y_dtype, for any M, N >= 1 and 1 <= K <= Q4_INT8_MAX_K.
+ * the sum in 32-bit integers (exact), then binary32 (the sum times the product
+ * of the two scales, plus the bias, each rounded) and one rounding to y_dtype,
+ * for any M, N >= 1 and 1 <= K <= Q4_INT8_MAX_K.
  *   A, W   device, int8, 16-byte aligned, rows lda / ldw bytes apart
  *          (multiples of 16, >= K); what lies past K is not read into a sum.
  *   bias   device, [N] of bias_dtype (Q4_F16 / Q4_BF16 / Q4_F32), or NULL.
@@ -462,8 +463,9 @@ Q4_API int q4_kv_dequantize(const q4_kv_cache *cache, const int64_t *slots, int6
  *   max_q  the most rows of any sequence: it only helps to choose the kernel.
  *   workspace  as q4_int8_gemm's, q4_kv_attention_workspace_size() bytes (the
  *          two may share one).
- * Entries outside the cache, lengths outside the table and row ranges outside
- * Q are cut off and set Q4_STATUS_INDEX.  The order of every sum is fixed by
+ * batch at most 65535.  Entries outside the cache, lengths outside the table
+ * and row ranges outside Q are cut off and set Q4_STATUS_INDEX; where ranges
+ * overlap, the rows of either may be left out.  The order of every sum is fixed by
  * the arguments and the device: identical calls give identical bits.
  */
 Q4_API int q4_kv_attention_workspace_size(const q4_kv_cache *cache, int64_t batch, int64_t total_q, int32_t q_heads,
@@ -481,13 +483,14 @@ Q4_API int q4_kv_attention(const q4_kv_cache *cache, const void *Q, int32_t dtyp
  * this call, process-wide; 0 restores the default of 2 s.  A wait that runs
  * out raises Q4_STATUS_TIMEOUT: the kernel stops, waits for its own copies
  * in flight and returns, leaving its outputs undefined.  After a timeout the
- * GEMV or grouped-quantize workspace must be zero-filled again before its
- * next use.  Host only; no device needed. */
+ * workspace of the call (of the 8-bit product and the cache attention its
+ * head) must be zero-filled again before its next use.  Host only; no device
+ * needed. */
 Q4_API int q4_set_wait_limit_ns(uint64_t ns);
 
 /* Test hook for the bounded waits, process-wide: while `on` is non-zero the
- * copy warp of the decode GEMV, the GEMM and the grouped quantize issues no
- * copies, so every compute warp's wait for a stage runs out after the wait
+ * copy warp of the decode GEMV, the GEMM, the grouped quantize and the 8-bit
+ * product issues no copies, and the cache attention brings in no keys, so every compute warp's wait for a stage runs out after the wait
  * limit (set a short one first) and the call returns with
  * Q4_STATUS_TIMEOUT and undefined outputs.  Leave it off otherwise.  Host
  * only. */

@@ -508,3 +508,65 @@ def test_an_attention_block_in_a_graph_and_on_streams(q4):
     torch.cuda.synchronize()
     assert all(torch.equal(u, v) for u, v in zip(got, want))
     assert q4.last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows", [2, 14, 150])
+def test_queries_that_are_not_finite_spoil_their_own_rows(q4, rows, dtype):
+    g = torch.Generator().manual_seed(rows)
+    c, table = fill_cache(q4, g, [500], 2, 128, 64, 64)
+    q = torch.randn(rows, 4, 128, generator=g).to(dtype).cuda()
+    args = (c, table.cuda(), torch.tensor([500], dtype=torch.int32, device="cuda"),
+            torch.tensor([0, rows], dtype=torch.int32, device="cuda"))
+    _, _, tol, _ = reference(c, table, [500], [rows], q, 128 ** -0.5, True, 0)
+    want = q4.kv_attention(q, *args)
+    bad = torch.zeros(rows, 4, dtype=torch.bool)
+    for row, head, value in ((0, 1, math.nan), (rows // 2, 3, math.inf), (rows - 1, 0, -math.inf)):
+        q[row, head, 5] = value
+        bad[row, head] = True
+    out = q4.kv_attention(q, *args).cpu()
+    assert torch.isnan(out[bad]).all()
+    # the others: both within the bound (the reference of a softmax may move at another unit of keys)
+    off, tol = (out.double() - want.cpu().double()).abs(), 2 * (tol + HALF[dtype] * (want.cpu().double().abs() + tol) + 2.0 ** -25)
+    assert (off <= tol)[~bad].all()
+
+
+def test_row_ranges_that_overlap_leave_the_workspace_usable(q4):
+    """The second range begins before the first ends: more row tiles than rows.  No result is promised, but the next
+    call's is right."""
+    g = torch.Generator().manual_seed(5)
+    rows, length = 2432, 20000  # 38 tiles of 256 rows for each of the four ranges: past the SMs by a few
+    c, table = fill_cache(q4, g, [length], 1, 64, 64, 64)
+    q = torch.randn(rows, 4, 64, generator=g).half().cuda()
+    args = (q, c, table.cuda().expand(8, -1), torch.full((8,), length, dtype=torch.int32, device="cuda"))
+    fine = torch.arange(9, dtype=torch.int32, device="cuda") * (rows // 8)
+    over = torch.tensor([0, rows] * 4 + [0], dtype=torch.int32, device="cuda")
+    for max_q in (8, rows):
+        want = q4.kv_attention(*args, fine, max_q)
+        q4.kv_attention(*args, over, max_q)
+        q4.clear_device_status()
+        assert torch.equal(q4.kv_attention(*args, fine, max_q), want)
+        assert q4.last_device_status() == 0
+
+
+@pytest.mark.parametrize("rows,length", [(1, 100), (3, 40000), (300, 700), (130, 30000)])
+def test_wait_limit_times_out_and_recovers(q4, rows, length):
+    """With the copy-stall hook on no keys arrive: the waits run out, the call reports it, and after the workspaces are
+    zeroed again the next call is right (whole segments and parts that are joined, both kernels)."""
+    g = torch.Generator().manual_seed(rows)
+    c, table = fill_cache(q4, g, [length], 1, 64, 64, 64)
+    q = torch.randn(rows, 2, 64, generator=g).half()
+    args = (q.cuda(), c, table.cuda(), torch.tensor([length], dtype=torch.int32, device="cuda"),
+            torch.tensor([0, rows], dtype=torch.int32, device="cuda"))
+    try:
+        q4.set_wait_limit_ns(200_000)
+        q4.set_copy_stall(True)
+        q4.kv_attention(*args)
+        torch.cuda.synchronize()
+        assert q4.last_device_status() & 2  # Q4_STATUS_TIMEOUT
+    finally:
+        q4.set_copy_stall(False)
+        q4.set_wait_limit_ns(0)
+        q4.reset_workspaces()
+        q4.clear_device_status()
+    check(q4, c, table, [length], [rows], q, implicit=False)
