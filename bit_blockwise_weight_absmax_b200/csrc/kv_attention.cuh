@@ -195,6 +195,18 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
   for (int mt = 0; mt < 2; ++mt) {
     float acc[NT][NB][4];
     uint32_t wa[W4], wb[W4];
+    // Inside a sequence the codes themselves: the zero-point's part, taken off
+    // afterwards, is some times the score, and the roundings of the sums average
+    // out over many keys.  Over few they do not, so units at the ends multiply
+    // code - 8, near the differences code - z (one to three keys: log sum exp
+    // off by 4e-7 of its size instead of 1.4e-6).
+    auto operand = [&](uint32_t w, bool high) -> uint32_t {
+      const uint32_t v = w & (high ? 0x00F000F0u : 0x000F000Fu);
+      if (inside) return v;
+      const uint32_t u = v | 0x64006400u;  // 1024 + v
+      const __half2 c = __hadd2(*reinterpret_cast<const __half2 *>(&u), __half2half2(__ushort_as_half(high ? 0xE480 : 0xE408)));
+      return *reinterpret_cast<const uint32_t *>(&c);
+    };
     const uint8_t *ra = kc + (16 * mt + g) * (D / 2) + t * (W4 * 4);
     if constexpr (W4 == 4) {
       const uint4 a = *reinterpret_cast<const uint4 *>(ra), bb = *reinterpret_cast<const uint4 *>(ra + 8 * (D / 2));
@@ -212,15 +224,15 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint4 q = *reinterpret_cast<const uint4 *>(s_q + (8 * n + g) * Sh::kQRow + (W4 * t + w) * 16);
-        if (w < NB) mma_f16_first(acc[n][j], wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u, wb[w] & 0x00F000F0u, q.x, q.y);
-        else mma_f16(acc[n][j], wa[w] & 0x000F000Fu, wb[w] & 0x000F000Fu, wa[w] & 0x00F000F0u, wb[w] & 0x00F000F0u, q.x, q.y);
-        mma_f16(acc[n][j], a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u, b8 & 0x00F000F0u, q.z, q.w);
+        if (w < NB) mma_f16_first(acc[n][j], operand(wa[w], false), operand(wb[w], false), operand(wa[w], true), operand(wb[w], true), q.x, q.y);
+        else mma_f16(acc[n][j], operand(wa[w], false), operand(wb[w], false), operand(wa[w], true), operand(wb[w], true), q.x, q.y);
+        mma_f16(acc[n][j], operand(a8, false), operand(b8, false), operand(a8, true), operand(b8, true), q.z, q.w);
       }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int kk = 16 * mt + g + 8 * h;
-      float sk[NB], sz[NB];
+      float sk[NB], kz[NB];
       uint32_t ka[NB], va[NB];
       if constexpr (NB == 2) {
         const uint2 u = *reinterpret_cast<const uint2 *>(ks + kk * 8), w = *reinterpret_cast<const uint2 *>(vs + kk * 8);
@@ -231,17 +243,20 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const float2 k2 = half_pair(ka[j]);
-        sk[j] = k2.x, sz[j] = k2.x * k2.y;
+        sk[j] = k2.x, kz[j] = inside ? k2.y : k2.y - 8.0f;
         sv[mt][h][j] = half_pair(va[j]).x;
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float s = sk[0] * acc[n][0][2 * h + e];
-          if constexpr (NB == 2) s = fmaf(sk[1], acc[n][1][2 * h + e], s);
-#pragma unroll
-          for (int j = 0; j < NB; ++j) s = fmaf(-sz[j], run.qs[n][j][e], s);
+          // the zero-point first: it cancels most of the sum of codes
+          auto block = [&](int j) {
+            const float a = acc[n][j][2 * h + e];
+            return fmaf(-kz[j], run.qs[n][j][e], inside ? a : a * 5.9604644775390625e-08f);  // 2^-24, as the codes
+          };
+          float s = sk[0] * block(0);
+          if constexpr (NB == 2) s = fmaf(sk[1], block(1), s);
           xs[mt][n][2 * h + e] = s;
         }
     }

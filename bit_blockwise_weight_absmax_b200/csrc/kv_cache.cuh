@@ -124,28 +124,42 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const __grid_cons
   }
 }
 
-// Eight codes of a word as binary16 s (code - z), pairs in the order of the
-// nibbles 04 15 26 37: 1024 + code is one masked OR, the difference exact, the
-// product rounded once.  z64 = -(64 + z), z1024 = -(1024 + z), both pairs.
-__device__ __forceinline__ uint4 kv_word(uint32_t w, __half2 s, __half2 z64, __half2 z1024) {
+// Eight codes of a word as binary16 code - z, pairs in the order of the nibbles
+// 04 15 26 37: 1024 + code is one masked OR, the difference exact.
+// z64 = -(64 + z), z1024 = -(1024 + z), both pairs.
+struct KvDiff {
+  __half2 d[4];
+};
+__device__ __forceinline__ KvDiff kv_diff(uint32_t w, __half2 z64, __half2 z1024) {
   const __half2 sixteenth = __half2half2(__ushort_as_half(0x2C00));  // 1 / 16
   auto h2 = [](uint32_t v) { return *reinterpret_cast<__half2 *>(&v); };
-  auto u2 = [](__half2 v) { return *reinterpret_cast<uint32_t *>(&v); };
   const uint32_t w8 = w >> 8;
-  uint4 r;
-  r.x = u2(__hmul2(__hadd2(h2((w & 0x000F000Fu) | 0x64006400u), z1024), s));
-  r.y = u2(__hmul2(__hfma2(h2((w & 0x00F000F0u) | 0x64006400u), sixteenth, z64), s));
-  r.z = u2(__hmul2(__hadd2(h2((w8 & 0x000F000Fu) | 0x64006400u), z1024), s));
-  r.w = u2(__hmul2(__hfma2(h2((w8 & 0x00F000F0u) | 0x64006400u), sixteenth, z64), s));
+  KvDiff r;
+  r.d[0] = __hadd2(h2((w & 0x000F000Fu) | 0x64006400u), z1024);
+  r.d[1] = __hfma2(h2((w & 0x00F000F0u) | 0x64006400u), sixteenth, z64);
+  r.d[2] = __hadd2(h2((w8 & 0x000F000Fu) | 0x64006400u), z1024);
+  r.d[3] = __hfma2(h2((w8 & 0x00F000F0u) | 0x64006400u), sixteenth, z64);
   return r;
 }
-// s d - r for the differences d and their rounded products r: exact.
-__device__ __forceinline__ uint4 kv_rest(uint4 d, __half2 s, uint4 r) {
-  auto rest = [&](uint32_t a, uint32_t b) {
-    const __half2 v = __hfma2(*reinterpret_cast<__half2 *>(&a), s, __hneg2(*reinterpret_cast<__half2 *>(&b)));
-    return *reinterpret_cast<const uint32_t *>(&v);
-  };
-  return make_uint4(rest(d.x, r.x), rest(d.y, r.y), rest(d.z, r.z), rest(d.w, r.w));
+// Their products with s, rounded once.
+__device__ __forceinline__ uint4 kv_scaled(const KvDiff &v, __half2 s) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 r = __hmul2(v.d[i], s);
+    o[i] = *reinterpret_cast<const uint32_t *>(&r);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// What that rounding left over: s d minus the rounded product, exact.
+__device__ __forceinline__ uint4 kv_rest(const KvDiff &v, __half2 s) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 r = __hfma2(v.d[i], s, __hneg2(__hmul2(v.d[i], s)));
+    o[i] = *reinterpret_cast<const uint32_t *>(&r);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 // -(64 + z) and -(1024 + z) of a state's word, in pairs.
 __device__ __forceinline__ __half2 kv_z64(__half2 state) {
@@ -192,7 +206,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_dequantize_kernel(const __grid_
     // binary16: the products themselves; bf16: the exact differences, times s
     // in binary32
     const __half2 s = DT == Q4_F16 ? __low2half2(sz) : __half2half2(__ushort_as_half(0x3C00));
-    uint4 r = kv_word(word[k], s, kv_z64(sz), kv_z1024(sz));  // pairs 04 15 26 37
+    const uint4 r = kv_scaled(kv_diff(word[k], kv_z64(sz), kv_z1024(sz)), s);  // pairs 04 15 26 37
     uint4 o;
     if constexpr (DT == Q4_F16) {
       o.x = __byte_perm(r.x, r.y, 0x5410), o.y = __byte_perm(r.z, r.w, 0x5410);

@@ -39,14 +39,13 @@ constexpr int kKpRows = 256;   // query rows of a CTA
 constexpr int kKpKeys = 128;   // keys of a tile
 constexpr int kKpThreads = 512;
 constexpr int kKpMinTiles = 4;         // key tiles a CTA takes of a tile that several share, at least
-constexpr int kKpExact = 16;           // CTAs of up to this many key tiles multiply the keys unrounded
 constexpr float kKpAhead = 14.0f;    // scores up to this far past the reference keep it
 constexpr float kKpMost = 32768.0f;  // of a row's weights in a tile: each is inside binary16 then
 
 template <int D> struct KpShape {
   static constexpr int kHalves = D / 64;                       // 128-byte wide parts of a row
   static constexpr int kTile = kHalves * kKpKeys * 128;        // a key or value tile, also 128 query rows
-  static constexpr int kSmem = 2 * kTile + 4 * kTile + kTile + 1024;  // queries, two stages of keys and values, key remainders
+  static constexpr int kSmem = 2 * kTile + 5 * kTile + 1024;  // queries; keys, values and the keys' remainders
 };
 
 // 32 columns of this warp's 32 lanes of tensor memory, without waiting.
@@ -117,8 +116,10 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t *s_qt = smem;                  // [2 halves of rows][kTile]
-  uint8_t *s_kv = smem + 2 * Sh::kTile;  // [2 stages][keys, values][kTile]
-  uint8_t *s_lo = smem + 6 * Sh::kTile;  // what rounding the keys to binary16 left over (one stage)
+  // [2 stages][keys, values][kTile], then what rounding the keys to binary16
+  // left over (one stage: two, with one of values, took 694 us instead of 650)
+  uint8_t *s_kv = smem + 2 * Sh::kTile;
+  auto rest_of = [](int stage) { return (4 - 2 * stage) * Sh::kTile; };  // from a stage's keys to their remainders
   __shared__ uint64_t s_bar[18];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_where[4];  // [3]: this CTA joins the parts
@@ -222,11 +223,12 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     tile0 = lo_first / kKpKeys;
     tiles = max(0, (hi_last + kKpKeys - 1) / kKpKeys - tile0);
   }
-  // s (q - z) has up to 15 bits, binary16 holds 11: over many keys the
-  // roundings average out of a row's sum, over few they would show in it (log
-  // sum exp off by 2e-4 for a row of one key).  CTAs of few keys multiply the
-  // remainders too.
-  const bool exact = uniform(tiles) <= kKpExact;
+  // s (q - z) has up to 15 bits, binary16 holds 11.  The output is rounded to
+  // 16 bits itself and hardly shows it (relative error 2.1e-4 with exact keys,
+  // 2.3e-4 with rounded ones, binary16), but the log sum exp does: 2e-6 over
+  // 2000 keys, 2e-4 over one.  Where it is asked for, the remainders are
+  // multiplied too: 1e-7.
+  const bool exact = p.lse != nullptr;
   // this CTA's part of the keys
   const int parts = (int)blockIdx.x < whole ? 1 : max(1, min(share, tiles / kKpMinTiles));
   if (part >= parts) {
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
       }
     };
     auto finish_lse = [&] {
-      if (p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m + __log2f(l)) * 0.69314718055994531f;
+      if (p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m + log2f(l)) * 0.69314718055994531f;
     };
     auto output = [&](int c, float (&o)[32]) {  // columns 32 c .. from tensor memory
       uint32_t t[32];
@@ -517,6 +519,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     auto store = [&](auto remainder, int which, int stage, bool poison) {
       // the row's base with the swizzle's XOR in it: chunk c lies at base ^ 16 c
       const uint32_t dst = smem_u32(s_kv + (stage * 2 + which) * Sh::kTile + kk * 128) + ((kk & 7) << 4);
+      const uint32_t to_rest = rest_of(stage);
       __half2 s[NB], z64[NB], z1024[NB];
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
@@ -533,12 +536,9 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
         for (int e = 0; e < 4; ++e) {
           const int w = 4 * v + e, n = w % NB;
           const uint32_t at = (dst ^ ((w & 7) << 4)) + (w >> 3) * (kKpKeys * 128);
-          const uint4 r = kv_word(w4[e], s[n], z64[n], z1024[n]);
-          st_shared_v4(at, r);
-          if constexpr (decltype(remainder)::value) {
-            const uint4 d = kv_word(w4[e], __half2half2(__ushort_as_half(0x3C00)), z64[n], z1024[n]);  // code - z
-            st_shared_v4(at + smem_u32(s_lo) - smem_u32(s_kv + (stage * 2 + which) * Sh::kTile), kv_rest(d, s[n], r));
-          }
+          const KvDiff d = kv_diff(w4[e], z64[n], z1024[n]);
+          st_shared_v4(at, kv_scaled(d, s[n]));
+          if constexpr (decltype(remainder)::value) st_shared_v4(at + to_rest, kv_rest(d, s[n]));
         }
       }
       fence_proxy_async_smem();
@@ -558,8 +558,8 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
         const uint32_t bad = __ballot_sync(0xffffffffu, bad_page);
         if (lane == 0) reinterpret_cast<uint32_t *>(&s_bad[j & 3])[warp - 8] = bad;
         if (!mbar_wait_warp(k_empty(st), ((j >> 1) & 1) ^ 1, p.status, abort, p.wait_ns)) break;
-        // the one stage of remainders: the tile before has been multiplied
-        if (decltype(exact_tag)::value && j > 0 && !mbar_wait_warp(k_empty(st ^ 1), ((j - 1) >> 1) & 1, p.status, abort, p.wait_ns)) break;
+        // the tile before has been multiplied, its remainders too
+        if (exact_tag && j > 0 && !mbar_wait_warp(k_empty(st ^ 1), ((j - 1) >> 1) & 1, p.status, abort, p.wait_ns)) break;
         store(exact_tag, 0, st, poison);
         if (lane == 0) mbar_arrive(k_full(st));
         if (!mbar_wait_warp(v_empty(st), ((j >> 1) & 1) ^ 1, p.status, abort, p.wait_ns)) break;
@@ -578,8 +578,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
       constexpr uint32_t id_o = umma_idesc_f16(0, 128, D) | kUmmaTransposeB;
       const uint32_t q0 = smem_u32(s_qt), kv0 = smem_u32(s_kv);
       const uint32_t lead = lane == 0;
-      const uint32_t dq = desc_lo_k(q0), dk = desc_lo_k(kv0), dv = desc_lo_mn(kv0 + Sh::kTile, kKpKeys * 128),
-                     dl = desc_lo_k(smem_u32(s_lo));
+      const uint32_t dq = desc_lo_k(q0), dk = desc_lo_k(kv0), dv = desc_lo_mn(kv0 + Sh::kTile, kKpKeys * 128);
       auto scores = [&](auto exact_tag, int half, int st) {
         const uint32_t a0 = dq + half * (Sh::kTile >> 4), b0 = dk + st * (2 * Sh::kTile >> 4);
 #pragma unroll
@@ -591,7 +590,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = ((k >> 2) * (kKpKeys * 128) + (k & 3) * 32) >> 4;
-            umma_f16_ss(s_addr + half * 128, a0 + off, dl + off, id_s, true, lead);
+            umma_f16_ss(s_addr + half * 128, a0 + off, b0 + (rest_of(st) >> 4) + off, id_s, true, lead);
           }
         }
       };

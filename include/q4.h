@@ -459,7 +459,9 @@ Q4_API int q4_kv_dequantize(const q4_kv_cache *cache, const int64_t *slots, int6
  * j > p - w.  A row that attends to nothing gives zeros and lse -inf.
  *   out    device, [total_q][q_heads][head_dim] packed, of `dtype`.
  *   lse    device, float [total_q][q_heads], log sum exp of the scaled
- *          scores, or NULL.
+ *          scores, or NULL.  Where it is asked for, prompts multiply the keys
+ *          with all their bits (else rounded to binary16, a fifth faster over
+ *          long ones): `out` may differ in its last bits between the two.
  *   max_q  the most rows of any sequence: it only helps to choose the kernel.
  *   workspace  as q4_int8_gemm's, q4_kv_attention_workspace_size() bytes (the
  *          two may share one).
