@@ -76,6 +76,10 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnParams &p, int b) {
 constexpr int kKvUnit = 32;    // keys per unit
 constexpr int kKvWarps = 8;
 constexpr int kKvSegmentCost = 24;  // of a segment in units of the list, beside its units
+// Segments of up to this many units a warp are not cut, where there are CTAs
+// enough (us, whole / cut: one sequence of 500 keys 10.7 / 13.3, of 777 13.5 /
+// 13.4, four of up to 100 9.6 / 13.4; a join costs what four more units do).
+constexpr int kKvWholeTurns = 3;
 constexpr float kKvMasked = -3.4028235e38f;  // in the place of a score that does not count
 constexpr int kKvAttnThreads = kKvWarps * 32;
 constexpr size_t kKvCountBytes = Q4_WORKSPACE_HEAD;
@@ -459,7 +463,8 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   __shared__ float s_hf[R], s_qs[NB][R];
   __shared__ int s_hi[R], s_lo[R];
   __shared__ int64_t s_scan[kKvWarps], s_first[2];
-  __shared__ int s_segs[kKvWarps], s_abort;
+  __shared__ int2 s_segs[kKvWarps];
+  __shared__ int s_abort;
   __shared__ unsigned s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -477,29 +482,31 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   __shared__ KvSpan s_span[kKvAttnThreads];
   const int per = (p.batch + kKvAttnThreads - 1) / kKvAttnThreads;
   int64_t mine = 0;
-  int segs = 0;
+  int my_segs = 0, longest = 0;
   for (int b = tid * per; b < min(p.batch, (tid + 1) * per); ++b) {
     const KvSpan v = kv_span<R>(p, b, group);
     if (per == 1) s_span[b] = v;
     mine += (int64_t)v.rt * p.c.heads * v.cost;
-    segs += min(v.rt, 1 << 16) * p.c.heads;
+    my_segs = min(my_segs + min(v.rt, 1 << 16) * p.c.heads, 1 << 20);
+    longest = max(longest, v.units);
   }
   int64_t incl = mine;
+  int incl_segs = my_segs;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += u;
+    const int v = __shfl_up_sync(0xffffffffu, incl_segs, o);
+    if (lane >= o) incl += u, incl_segs = min(incl_segs + v, 1 << 20);
   }
-  segs = min(segs, 1 << 20);
-  segs = __reduce_add_sync(0xffffffffu, segs);
-  if (lane == 31) s_scan[warp] = incl, s_segs[warp] = min(segs, 1 << 20);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) s_scan[warp] = incl, s_segs[warp] = make_int2(incl_segs, longest);
   __syncthreads();
   int64_t before = 0, total = 0;
-  segs = 0;
+  int before_segs = 0, segs = 0;
   for (int w = 0; w < kKvWarps; ++w) {
-    if (w < warp) before += s_scan[w];
+    if (w < warp) before += s_scan[w], before_segs += s_segs[w].x;
     total += s_scan[w];
-    segs += s_segs[w];
+    segs += s_segs[w].x, longest = max(longest, s_segs[w].y);
   }
   incl += before;
   if (total == 0) return;
@@ -508,7 +515,12 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   // CTAs: equal ones are then cut alike, and none lies in two pieces of a CTA
   const int grid = min((int)gridDim.x, Sh::kFactors);
   int ctas = (int)min((int64_t)grid, (total + kKvWarps - 1) / kKvWarps);
-  if (segs <= grid) {
+  // short segments, a CTA for each: as if they all had the longest's cost
+  const int uniform = segs <= grid && longest <= kKvWholeTurns * kKvWarps ? longest : 0;
+  if (uniform) {
+    mine = (int64_t)my_segs * uniform, incl = (int64_t)(before_segs + incl_segs) * uniform, total = (int64_t)segs * uniform;
+    ctas = segs;
+  } else if (segs <= grid) {
     const int each = (int)min((int64_t)(grid / segs), kv_div(total + kKvWarps * segs - 1, kKvWarps * segs));
     if (each * segs * 16 >= grid * 15 || ctas < grid) ctas = each * segs;
   }
@@ -527,7 +539,11 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
   KvSegment<R> sg;
   sg.b = (int)s_first[0];
   sg.base = s_first[1];
-  auto span_of = [&](int b) { return per == 1 ? s_span[b] : kv_span<R>(p, b, group); };
+  auto span_of = [&](int b) {
+    KvSpan v = per == 1 ? s_span[b] : kv_span<R>(p, b, group);
+    if (uniform) v.cost = uniform;
+    return v;
+  };
   sg.v = span_of(sg.b);
   // sg: the segment that unit x of the list belongs to, as far as this CTA
   // takes it, and x past it; false where the run has no more
