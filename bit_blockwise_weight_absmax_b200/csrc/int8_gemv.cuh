@@ -7,7 +7,8 @@
 // the tokens' maximum, so the quantization (every CTA repeats it: 2 M K bytes
 // from L2) hides behind the weights' way from memory.  Sums are dot products
 // of four bytes (dp4a) in 32-bit integers, joined over the warp by shuffles:
-// no partial tile, no workspace, one launch instead of two.
+// no partial tile, no workspace, one launch instead of two.  One token: 4096 x
+// 4096 6.4 us (2.6 TB/s), 28672 x 8192 39 us (6.0 TB/s).
 // More tokens than four are better on the tensor cores (int8_gemm.cuh): the
 // dot products and the tokens' shared-memory reads grow with them.
 #pragma once

