@@ -16,6 +16,7 @@ inline bool in16(int d) { return d == Q4_F16 || d == Q4_BF16; }
 inline bool any_float(int d) { return d == Q4_F16 || d == Q4_BF16 || d == Q4_F32; }
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 constexpr int64_t kMaxRows = INT32_MAX;
+constexpr int64_t kMaxKeys = (int64_t)1 << 30;  // of a sequence: positions and windows stay within 32 bits
 constexpr int kDefaultSms = 148;  // sizes asked for without a device are those of a B200
 int plan_sms() {
   const DeviceInfo di = device_info();
@@ -225,7 +226,7 @@ int q4_kv_attention(const q4_kv_cache *cache, const void *Q, int32_t dtype, int6
   rc = q4_kv_attention_workspace_size(cache, batch, total_q, q_heads, &need);
   if (rc != Q4_OK) return rc;
   if ((!cu_q && total_q != batch) || max_q < 1 || window < 0 || table_pages < 1 || table_pages > INT32_MAX || table_stride < table_pages ||
-      table_pages * cache->page_size > INT32_MAX - 65536 || q_token_stride < 0 || q_head_stride < 0)
+      table_pages * cache->page_size > kMaxKeys || q_token_stride < 0 || q_head_stride < 0)
     return Q4_ERR_SHAPE;
   if (!aligned16(Q) || !aligned16(out) || q_token_stride % 8 || q_head_stride % 8 || !aligned16(workspace)) return Q4_ERR_ALIGN;
   if (need && (!workspace || workspace_bytes < need)) return Q4_ERR_WORKSPACE;
@@ -239,7 +240,9 @@ int q4_kv_attention(const q4_kv_cache *cache, const void *Q, int32_t dtype, int6
   p.batch = (int32_t)batch, p.total_q = (int32_t)total_q, p.q_heads = q_heads;
   p.scale = scale;
   p.causal = causal;
-  p.window = (int32_t)std::min<int64_t>(window, INT32_MAX);
+  // a window as long as the table holds every key (and far ones would overflow
+  // the kernels' 32-bit positions)
+  p.window = window >= table_pages * cache->page_size ? 0 : (int32_t)window;
   p.out = (uint16_t *)out;
   p.lse = lse;
   p.counts = (unsigned *)workspace;

@@ -452,11 +452,12 @@ Q4_API int q4_kv_dequantize(const q4_kv_cache *cache, const int64_t *slots, int6
  *   lens   device, int32 [batch]: keys of each sequence, its query rows' own
  *          included (append first); 0 is allowed.
  *   table  device, int32 [batch][table_stride], its first table_pages columns
- *          valid: page of each page_size keys.  Entries past a length are not
- *          read.
+ *          valid: page of each page_size keys (2^30 keys at most).  Entries
+ *          past a length are not read.
  * Row i of n stands at position p = len - n + i and attends to the keys
  * j <= p (causal 1) or to all (causal 0), and with window w > 0 only to
- * j > p - w.  A row that attends to nothing gives zeros and lse -inf.
+ * j > p - w.  A row that attends to nothing gives zeros and lse -inf; one
+ * whose scaled scores leave binary32's range gives NaN.
  *   out    device, [total_q][q_heads][head_dim] packed, of `dtype`.
  *   lse    device, float [total_q][q_heads], log sum exp of the scaled
  *          scores, or NULL.  Where it is asked for, prompts multiply the keys

@@ -570,3 +570,16 @@ def test_wait_limit_times_out_and_recovers(q4, rows, length):
         q4.reset_workspaces()
         q4.clear_device_status()
     check(q4, c, table, [length], [rows], q, implicit=False)
+
+
+@pytest.mark.parametrize("rows", [1, 9, 200])
+def test_windows_longer_than_every_sequence_are_none(q4, rows):
+    """The first rows stand in front of position 0, where a far window's begin would leave 32 bits."""
+    g = torch.Generator().manual_seed(rows)
+    lens, qs = [rows, max(rows - 5, 1)], [rows, rows]
+    c, table = fill_cache(q4, g, lens, 2, 64, 64, 16)
+    q = torch.randn(2 * rows, 4, 64, generator=g).half()
+    want = check(q4, c, table, lens, qs, q, implicit=False)
+    for window in (rows, 10 ** 6, 2 ** 31 - 1, 2 ** 40):
+        got = check(q4, c, table, lens, qs, q, window=window, implicit=False)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) or window == rows  # cut at other keys, it may round otherwise
