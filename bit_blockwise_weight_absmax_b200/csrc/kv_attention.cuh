@@ -78,7 +78,10 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnParams &p, int b) {
 
 constexpr int kKvUnit = 32;    // keys per unit
 constexpr int kKvWarps = 8;
-constexpr int kKvSegmentCost = 24;  // of a segment in units of the list, beside its units
+// Of a segment in units of the list, beside its units: its begin and join (us
+// at 16 / 24 / 32 / 40: 16 sequences 46.0 / 45.6 / 45.1 / 46.1, 24 of five
+// drafted tokens 24.4 / 21.5 / 20.6 / 18.6, 64 of 4096 keys 71 / 68 / 69 / 71).
+constexpr int kKvSegmentCost = 32;
 // Segments of up to this many units a warp are not cut, where there are CTAs
 // enough (us, whole / cut: one sequence of 500 keys 10.7 / 13.3, of 777 13.5 /
 // 13.4, four of up to 100 9.6 / 13.4; a join costs what four more units do).
