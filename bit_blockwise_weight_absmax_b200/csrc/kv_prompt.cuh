@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
       }
     };
     auto finish_lse = [&] {
-      if (p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m + log2f(l)) * 0.69314718055994531f;
+      // (a row whose scores are all NaN has no reference, and the sum NaN)
+      if (p.lse) p.lse[at] = l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) + log2f(l)) * 0.69314718055994531f;
     };
     auto output = [&](int c, float (&o)[32]) {  // columns 32 c .. from tensor memory
       uint32_t t[32];
