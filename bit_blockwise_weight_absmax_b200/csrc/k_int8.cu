@@ -114,9 +114,13 @@ namespace {
 template <int MT, int DT, bool VEC>
 int go_gemv(const I8GemvParams &p, int sms, cudaStream_t st) {
   const int smem = MT * ((p.K + 15) / 16 * 16);
+  // without the opt-in the static and the dynamic part together may not pass 48 KB
+  constexpr auto kern = int8_gemv_kernel<MT, DT, VEC>;
+  const int rc = set_smem_attr_once<kern>(kI8vMaxBytes, false);
+  if (rc != Q4_OK) return rc;
   // as many CTAs of 8 warps as the SMs hold, a warp for each row where there are fewer
   const int grid = (int)std::min<int64_t>((p.N + 7) / 8, (int64_t)i8v_ctas(MT) * sms);
-  launch_pdl(int8_gemv_kernel<MT, DT, VEC>, dim3((unsigned)grid), dim3(kI8vThreads), smem, st, p);
+  launch_pdl(kern, dim3((unsigned)grid), dim3(kI8vThreads), smem, st, p);
   return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
 }
 template <int DT, bool VEC>
