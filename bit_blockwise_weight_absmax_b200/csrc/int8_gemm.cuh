@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
     I8Walk w = i8_walk(p, c);
     I8Item it;
     uint32_t count = 0;
-    for (; !*abort && i8_next(p, w, g, it); ++count) {
+    for (; !__any_sync(0xffffffffu, *abort) && i8_next(p, w, g, it); ++count) {
       int tt, tn;
       i8_tile(p, it.tile, tt, tn);
       const int b = count & 1;

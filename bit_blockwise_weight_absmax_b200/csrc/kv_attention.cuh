@@ -147,6 +147,13 @@ __device__ __forceinline__ void kv_bulk_load(uint32_t dst, const void *src, uint
       : "memory");
 }
 
+// After a wait that ran out: waits for the `n` stages from use `no` on, whose
+// copies are on their way, so that they have landed before the CTA ends.
+static __device__ __noinline__ void kv_drain(uint32_t bar, uint32_t no, int n, int stages) {
+  volatile int no_abort = 0;
+  for (int s = 0; s < n; ++s) mbar_wait(bar + 8 * ((no + s) % stages), ((no + s) / stages) & 1, nullptr, &no_abort);
+}
+
 // a / b for a >= 0, b > 0: in 32 bits where they are enough.
 __device__ __forceinline__ int64_t kv_div(int64_t a, int b) {
   return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
@@ -591,8 +598,9 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
     return __ldg(table + (key >> p.c.page_log2));
   };
   uint32_t there = 0;  // bit stage * 2 + part: the part was copied
+  bool gave_up = false;  // a wait of this warp ran out: no more copies
   auto issue = [&](int key, int pg, uint32_t no) {
-    if (p.stall_copies) return;
+    if (p.stall_copies || gave_up) return;
     const int st = no % Sh::kStages;
     const bool good = pg >= 0 && pg < pages;
     if (!good && pg != kNoPage) raise_status(p.status, Q4_STATUS_INDEX);
@@ -696,9 +704,14 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
     }
 
     int key = sg.key0 + warp * kKvUnit;
-    for (int k = warp; k < sg.count; k += kKvWarps, ++seq_no, key += kKvWarps * kKvUnit) {
+    for (int k = warp; k < sg.count && !gave_up; k += kKvWarps, ++seq_no, key += kKvWarps * kKvUnit) {
       const int st = seq_no % Sh::kStages;
-      if (!mbar_wait(bar + 8 * st, (seq_no / Sh::kStages) & 1, p.status, &s_abort, p.wait_ns)) break;
+      // the whole warp goes on or none of it: what follows are its collectives
+      if (!__all_sync(0xffffffffu, mbar_wait(bar + 8 * st, (seq_no / Sh::kStages) & 1, p.status, &s_abort, p.wait_ns))) {
+        gave_up = true;
+        if (!p.stall_copies) kv_drain(bar, seq_no, min(Sh::kStages, (sg.count - k + kKvWarps - 1) / kKvWarps), Sh::kStages);
+        break;
+      }
       const uint32_t parts = (there >> (2 * st)) & 3u;
       const uint8_t *kc = ring + st * Sh::kStage;
       const bool inside = key >= sg.lo_all && key + kKvUnit <= sg.hi_all && parts == (part_log2 == 5 ? 1u : 3u);
@@ -881,12 +894,6 @@ __global__ void __launch_bounds__(kKvAttnThreads, KvShape<D, B, NT>::kCtas) kv_a
     }
     if (!more) break;
     __syncthreads();  // shared memory is free for the next segment
-  }
-  if (s_abort) {
-    // after a timeout the copies that nobody waits for get a millisecond
-    // (they take microseconds) before the CTA ends
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
   }
 }
 

@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     const uint64_t hf2 = f2_pack(hf, hf);
     bool ok = true, fresh = true;  // fresh: a row of the warp has no reference yet
     for (int j = 0; j < tiles && ok; ++j) {
-      if (!mbar_wait(s_full(half), j & 1, p.status, abort, p.wait_ns)) {
+      // the whole warp goes on or none of it: what follows are its collectives
+      if (!__all_sync(0xffffffffu, mbar_wait(s_full(half), j & 1, p.status, abort, p.wait_ns))) {
         ok = false;
         break;
       }
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
           if (move) m = top, l *= f;
           if ((j | u) && __any_sync(0xffffffffu, f != 1.0f)) {
             // the output so far takes the new reference, once its last product is in
-            ok = mbar_wait(pv_done(half, 1 - u), (j - 1 + u) & 1, p.status, abort, p.wait_ns);
+            ok = __all_sync(0xffffffffu, mbar_wait(pv_done(half, 1 - u), (j - 1 + u) & 1, p.status, abort, p.wait_ns));
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
