@@ -13,10 +13,13 @@
 //  - mma.sync m16n8k16, keys on the 16-row side, query rows (8 or 16 of the
 //    rows that share a kv head) on the 8-column side.  The contraction over d
 //    may run in any order, so a lane takes the words of a row as they lie.
-//  - Online softmax in base 2 with a running reference m near the maximum of
-//    score + log2(s_v), so that the weights w = 2^(score - m) s_v use binary16's
-//    range well whatever the values' sizes.  m moves only when a weight leaves
-//    that range (a packed maximum finds it), which is rare after the first
+//  - Online softmax in base 2 with a running reference m, kKvLift below the
+//    maximum of score + log2(s_v), so that the weights w = 2^(score - m) s_v use
+//    binary16's range well whatever the values' sizes: the largest is 2^10 when
+//    m is taken, and weights have all of binary16's bits down to 2^-24 of it and
+//    are dropped below 2^-35 (with the largest at 1, 131072 keys at 2^-25 counted
+//    in the sum and not in the output).  m moves only when a weight passes the
+//    range (a packed maximum finds it), which is rare after the first
 //    unit: no reduction over lanes and no rescaling in the common case.  The
 //    zero-points' sum is one more MMA with the weights.  Query rows are scaled
 //    by a power of two into binary16 (exact for both 16-bit types down to 2^-38
@@ -86,6 +89,7 @@ constexpr int kKvSegmentCost = 32;
 // enough (us, whole / cut: one sequence of 500 keys 10.7 / 13.3, of 777 13.5 /
 // 13.4, four of up to 100 9.6 / 13.4; a join costs what four more units do).
 constexpr int kKvWholeTurns = 3;
+constexpr float kKvLift = 10.0f;  // the largest weight when the reference is taken: 2^10, six binades below binary16's end
 constexpr float kKvMasked = -3.4028235e38f;  // in the place of a score that does not count
 constexpr int kKvAttnThreads = kKvWarps * 32;
 constexpr size_t kKvCountBytes = Q4_WORKSPACE_HEAD;
@@ -295,7 +299,7 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
       }
     }
   }
-  // the reference moves to the maximum so far of score + log2(s_v)
+  // the reference moves to kKvLift below the maximum so far of score + log2(s_v)
   auto move = [&] {
     run.pending = false;
 #pragma unroll
@@ -310,7 +314,7 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
             float top = sv[mt][h][0];
             if constexpr (NB == 2) top = fmaxf(top, sv[mt][h][1]);
             const float s = xs[mt][n][2 * h + e];
-            if (s != kKvMasked) to = fmaxf(to, fmaf(s, run.hf[n][e], fmaxf(lg2(top), -24.0f)));
+            if (s != kKvMasked) to = fmaxf(to, fmaf(s, run.hf[n][e], fmaxf(lg2(top), -24.0f) - kKvLift));
           }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));

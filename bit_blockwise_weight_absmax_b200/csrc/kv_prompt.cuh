@@ -9,8 +9,9 @@
 //                 tensor memory and writes the weights back in binary16 over
 //                 them.  The reference m of 2^(score - m) stays that of earlier
 //                 tiles while the weights fit binary16 (their sum tells); only
-//                 then, and for the first tile, the maximum is taken and the
-//                 output rescaled: one pass over the scores in the common case;
+//                 then, and for the first tile, the maximum is taken, the
+//                 reference set kKpLift below it and the output rescaled: one
+//                 pass over the scores in the common case;
 //   warps 8..11   dequantize: a thread owns a key.  Codes come straight from
 //                 global memory into registers, a tile ahead; 1024 + code is
 //                 one masked OR, minus 1024 + z exact, times s rounded once to
@@ -42,8 +43,12 @@ constexpr int kKpRows = 256;   // query rows of a CTA
 constexpr int kKpKeys = 128;   // keys of a tile
 constexpr int kKpThreads = 512;
 constexpr int kKpMinTiles = 4;         // key tiles a CTA takes of a tile that several share, at least
-constexpr float kKpAhead = 14.0f;    // scores up to this far past the reference keep it
-constexpr float kKpMost = 32768.0f;  // of a row's weights in a tile: each is inside binary16 then
+// The reference is taken kKpLift below the maximum: the largest weight is 2^8
+// then, those of 2^-22 of it have all of binary16's bits, and below 2^-33 they
+// are dropped (64 equal ones sum up to 2^14, well inside kKpMost).
+constexpr float kKpLift = 8.0f;
+constexpr float kKpAhead = 15.0f;    // scores up to this far past the reference keep it
+constexpr float kKpMost = 65504.0f;  // of a row's weights in a tile: each is inside binary16 then
 
 template <int D> struct KpShape {
   static constexpr int kHalves = D / 64;                       // 128-byte wide parts of a row
@@ -362,8 +367,9 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
           float top = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 64; ++k) top = fmaxf(top, __uint_as_float(s[k >> 5][k & 31]));
-          top = fmaxf(m, top * hf);
+          top *= hf;
           if (fresh) move = !(top <= m + kKpAhead);
+          top = fmaxf(m, top - kKpLift);
           const float f = !move || m == -INFINITY ? 1.0f : ex2(m - top);
           if (move) m = top, l *= f;
           if ((j | u) && __any_sync(0xffffffffu, f != 1.0f)) {

@@ -1,10 +1,11 @@
 """The 4-bit key/value cache and its attention on a B200 where they are easily wrong."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
-from test_kv_gpu import check, fill_cache, q4  # noqa: F401  (q4: the fixture)
+from test_kv_gpu import HALF, check, fill_cache, q4  # noqa: F401  (q4: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +67,63 @@ def test_waits_that_run_out_while_copies_are_on_their_way(q4, rows, length):
         q4.reset_workspaces()
         q4.clear_device_status()
     check(q4, c, table, [length], [rows], q, implicit=False)
+
+
+def one_large_weight(q4, D, length, gap, first):
+    """A cache whose first key's score lies 2^gap above all the others', which are zero, and whose first value is `first`
+    in elements 1, 4, 7, .. and the others' 15 in elements 0, 3, 6, ..: every number is an integer that the cache and binary16 hold exactly.
+    Returns the cache, its table, the query vector and the scale."""
+    page = 256
+    pages = (length + page - 1) // page
+    c = q4.kv_cache(pages, 1, D, page, 64)
+    k, v = torch.zeros(2, length, 1, D, dtype=torch.float16, device="cuda")
+    k[0, :, ::64] = 15
+    v[0, :, 1::3] = first
+    v[1:, :, ::3] = 15
+    q4.kv_append(c, k, v, torch.arange(length, device="cuda"))
+    query = torch.zeros(D, dtype=torch.float16, device="cuda")
+    query[0] = 1
+    return c, torch.arange(pages, dtype=torch.int32, device="cuda")[None], query, float(np.float32(gap * math.log(2) / 15))
+
+
+@pytest.mark.parametrize("first", [0, 15])
+@pytest.mark.parametrize("gap", [20.356, 25.1])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("batch,rows,group", [(300, 1, 1), (300, 1, 12), (1, 1024, 37), (1, 130, 1)])
+def test_many_small_weights_beside_a_large_one(q4, D, batch, rows, group, gap, first):
+    """131072 keys whose weights are 2^-gap of the first key's: none of them may be lost.  A weight's binary16 rounding
+    is half a step, 2^-11, or below the normal range 2^-25, where the largest weight is at least 2^8 (so 2^(gap - 33) of
+    it); binary32 sums of at most 8192 MMAs of 16 keys and 300 joined parts, terms of one sign, a step (2^-23, an MMA may
+    truncate) each; exponentials 2^-20."""
+    length = 131073
+    c, table, query, scale = one_large_weight(q4, D, length, gap, first)
+    q = query.expand(batch * rows, group, D).contiguous()
+    cu = torch.arange(batch + 1, dtype=torch.int32, device="cuda") * rows
+    out, lse = q4.kv_attention(q, c, table.expand(batch, -1).contiguous(), ints([length] * batch), cu, max_q=rows,
+                               scale=scale, return_lse=True)
+    tail = (length - rows + torch.arange(rows, dtype=torch.float64)) * 2.0 ** (-scale * 15 / math.log(2))  # of each row
+    share = (tail / (1 + tail))[None, :, None, None].cuda()
+    got = out.double().view(batch, rows, group, D)
+    sums = 8492 * 2.0 ** -23
+    rel = max(2.0 ** -11, 2.0 ** (gap - 33)) + 2 * sums + HALF[torch.float16] + 2.0 ** -19
+    for at, want in ((0, 15 * share), (1, first * (1 - share)), (2, 0 * share)):
+        assert ((got[..., at::3] - want).abs() <= rel * want + 2.0 ** -25).all()
+    wl = scale * 15 + torch.log1p(tail)[None, :, None].cuda()
+    # eight roundings of numbers up to 2^5 (the score, its factor and the reference in base 2), and the sum's
+    assert ((lse.double().view(batch, rows, group) - wl).abs() <= 8 * 2.0 ** -19 + sums).all()
+    assert q4.last_device_status() == 0
+
+
+@pytest.mark.parametrize("rows", [1, 5, 14, 140])
+def test_a_vector_whose_blocks_differ_in_size(q4, rows):
+    """The values of a vector's two blocks, 2^20 apart, are both right to their own size."""
+    g = torch.Generator().manual_seed(rows + 3)
+    n, D = 700, 128
+    c = q4.kv_cache(11, 2, D, 64, 64)
+    k, v = torch.randn(2, n, 2, D, generator=g)
+    v[:, :, :64] *= 2000
+    v[:, :, 64:] *= 2e-3
+    v[:, 1] = v[:, 1].roll(64, 1)
+    q4.kv_append(c, k.half().cuda(), v.half().cuda(), torch.arange(n).cuda())
+    check(q4, c, torch.arange(11, dtype=torch.int32)[None], [n], [rows], torch.randn(rows, 6, D, generator=g).bfloat16(),
+          implicit=False)
