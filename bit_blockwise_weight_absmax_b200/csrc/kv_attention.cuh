@@ -267,6 +267,10 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
         sk[j] = k2.x, kz[j] = inside ? k2.y : k2.y - 8.0f;
         sv[mt][h][j] = half_pair(va[j]).x;
       }
+      // NaN where a block of the value could not be held: its key's score is
+      // NaN then, and so is the whole row, log sum exp included
+      float spoil = sv[mt][h][0] * 0.0f;
+      if constexpr (NB == 2) spoil = fmaf(sv[mt][h][1], 0.0f, spoil);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -276,7 +280,7 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
             const float a = acc[n][j][2 * h + e];
             return fmaf(-kz[j], run.qs[n][j][e], inside ? a : a * 5.9604644775390625e-08f);  // 2^-24, as the codes
           };
-          float s = sk[0] * block(0);
+          float s = fmaf(sk[0], block(0), spoil);
           if constexpr (NB == 2) s = fmaf(sk[1], block(1), s);
           xs[mt][n][2 * h + e] = s;
         }

@@ -427,7 +427,8 @@ typedef struct {
  *          twice the cache holds either token's blocks, whole or mixed.
  * A block with an infinity or a NaN, or whose range max(x, 0) - min(x, 0)
  * exceeds 61440 (its values would leave binary16), is stored with s = NaN and
- * sets Q4_STATUS_NONFINITE: rows that attend to it give NaN.
+ * sets Q4_STATUS_NONFINITE: rows that attend to it give NaN, in every element
+ * and in the log sum exp.
  */
 Q4_API int q4_kv_append(const q4_kv_cache *cache, const void *K, const void *V, int32_t dtype, int64_t tokens,
                         int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,

@@ -127,3 +127,22 @@ def test_a_vector_whose_blocks_differ_in_size(q4, rows):
     q4.kv_append(c, k.half().cuda(), v.half().cuda(), torch.arange(n).cuda())
     check(q4, c, torch.arange(11, dtype=torch.int32)[None], [n], [rows], torch.randn(rows, 6, D, generator=g).bfloat16(),
           implicit=False)
+
+
+@pytest.mark.parametrize("D,B", [(64, 64), (128, 64), (128, 128)])
+@pytest.mark.parametrize("rows", [1, 5, 14, 150])
+@pytest.mark.parametrize("name", ["k_state", "v_state"])
+def test_a_block_that_could_not_be_held_spoils_whole_rows_in_either_kernel(q4, D, B, rows, name):
+    """Whichever block of the key or the value it is, and whichever kernel the hint chooses: the rows that attend to it
+    are NaN in every element and in the log sum exp, the others are not."""
+    g = torch.Generator().manual_seed(rows)
+    lens, qs = [260, 260], [rows, rows]
+    c, table = fill_cache(q4, g, lens, 2, D, B, 64)
+    getattr(c, name)[int(table[0, 1]), 1, 3, D // B - 1, 0] = math.nan  # key 67 of the first sequence, head 1
+    q = torch.randn(2 * rows, 4, D, generator=g).half().cuda()
+    for max_q in (1, rows, 1000):
+        out, lse = q4.kv_attention(q, c, table.cuda(), ints(lens), ints([0, rows, 2 * rows]), max_q=max_q, return_lse=True)
+        for t in (out[:rows, 2:], lse[:rows, 2:]):
+            assert torch.isnan(t).all()
+        for t in (out[:rows, :2], out[rows:], lse[:rows, :2], lse[rows:]):
+            assert torch.isfinite(t).all()
