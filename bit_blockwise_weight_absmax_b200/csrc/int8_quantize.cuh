@@ -6,7 +6,8 @@
 // pieces of it in registers between the maximum and the codes, so a row is
 // read from memory once; what a longer row has beyond that is read again
 // (from L2).  The quotient is the correctly rounded one (div_markstein, and
-// __fdiv_rn for scales outside its range).
+// __fdiv_rn for scales outside its range).  Rows of binary32 (weights at load
+// time) take a plain kernel of two passes.
 #pragma once
 #include "q4_common.cuh"
 
@@ -126,6 +127,42 @@ __global__ void __launch_bounds__(THREADS, kI8QuantThreads / THREADS) int8_quant
     if (i < pieces) store(i, keep[k]);
   }
   for (int i = tid + kI8Keep * THREADS; i < pieces; i += THREADS) store(i, load(i));
+  if (tid == 0) {
+    p.scale[row] = sc.stored;
+    if (sc.bad) raise_status(p.status, Q4_STATUS_NONFINITE);
+  }
+}
+
+// Rows of binary32, once at load time: a pass for the maximum, one for the
+// codes (from L2 where a row fits).  Magnitudes order as their bit patterns,
+// infinities and NaNs last.  A subnormal s is rounded so coarsely that x / s
+// may pass 127: clamped.
+struct I8QuantF32Params {
+  const float *X;
+  int64_t rows, ldx, ldc;
+  int32_t cols;
+  int8_t *codes;
+  float *scale;
+  int *status;
+};
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) int8_quantize_f32_kernel(const __grid_constant__ I8QuantF32Params p) {
+  pdl_launch_then_wait();
+  __shared__ uint32_t s_max[THREADS / 32];
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const float *x = p.X + row * p.ldx;
+  uint32_t m = 0;
+  for (int i = tid; i < p.cols; i += THREADS) m = max(m, __float_as_uint(__ldg(x + i)) & 0x7FFFFFFFu);
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((tid & 31) == 0) s_max[tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < THREADS / 32; ++j) m = max(m, s_max[j]);
+  const I8Scale sc = i8_scale(__uint_as_float(m));
+  int8_t *c = p.codes + row * p.ldc;
+  for (int i = tid; i < p.cols; i += THREADS)
+    c[i] = sc.zero ? (int8_t)0 : (int8_t)max(-127, min(127, __float2int_rn(__fdiv_rn(__ldg(x + i), sc.s))));
   if (tid == 0) {
     p.scale[row] = sc.stored;
     if (sc.bad) raise_status(p.status, Q4_STATUS_NONFINITE);

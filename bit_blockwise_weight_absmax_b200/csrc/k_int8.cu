@@ -54,6 +54,11 @@ int run_int8_quantize(int dt, const I8QuantParams &p, cudaStream_t st) {
   return vec ? go_quantize<Q4_BF16, true>(p, st) : go_quantize<Q4_BF16, false>(p, st);
 }
 
+int run_int8_quantize_f32(const I8QuantF32Params &p, cudaStream_t st) {
+  launch_pdl(int8_quantize_f32_kernel<256>, dim3((unsigned)p.rows), dim3(256), 0, st, p);
+  return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
+}
+
 // The plan is the cheapest by this estimate (us, fitted to the measured
 // products of 64 .. 4096 tokens by 300 .. 28672 rows, which it meets within
 // about 15 %): a fixed part (set-up, first copies, last epilogue), the

@@ -74,6 +74,23 @@ int q4_int8_quantize_rows(const void *X, int32_t x_dtype, int64_t rows, int64_t 
   return run_int8_quantize(x_dtype, p, (cudaStream_t)stream);
 }
 
+int q4_int8_quantize_rows_f32(const float *X, int64_t rows, int64_t cols, int64_t ldx, int8_t *codes, int64_t ldc,
+                              float *scale, void *stream) {
+  if (!X || !codes || !scale) return Q4_ERR_ARG;
+  if (rows < 1 || cols < 1 || rows > kMaxRows || cols > Q4_INT8_MAX_K || ldx < cols || ldc < cols || ldc % 16)
+    return Q4_ERR_SHAPE;
+  if (!aligned16(codes) || ((uintptr_t)X & 3u)) return Q4_ERR_ALIGN;
+  const DeviceInfo di = device_info();
+  if (di.ok != Q4_OK) return di.ok;
+  I8QuantF32Params p;
+  p.X = X;
+  p.rows = rows, p.ldx = ldx, p.ldc = ldc, p.cols = (int32_t)cols;
+  p.codes = codes;
+  p.scale = scale;
+  p.status = di.status;
+  return run_int8_quantize_f32(p, (cudaStream_t)stream);
+}
+
 int q4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes) {
   if (!bytes) return Q4_ERR_ARG;
   const int rc = check_linear(M, N, K);

@@ -23,6 +23,7 @@ struct I8Plan {
 };
 I8Plan int8_plan(int64_t M, int64_t N, int64_t K, int sms);
 int run_int8_quantize(int dt, const I8QuantParams &p, cudaStream_t st);
+int run_int8_quantize_f32(const I8QuantF32Params &p, cudaStream_t st);
 // Whether M tokens of K take the one-launch kernel of int8_gemv.cuh.
 bool int8_gemv_ok(int64_t M, int64_t K);
 int run_int8_gemv(int x_dtype, const I8GemvParams &p, int sms, cudaStream_t st);

@@ -41,7 +41,7 @@ class Linear8bit(torch.nn.Module):
             raise q4.Q4Error(f"Linear8bit cannot run this layer: {why}")
         w = lin.weight.detach()
         if w.dtype not in (torch.float16, torch.bfloat16):
-            w = w.to(torch.bfloat16)
+            w = w.float()
         codes, scale = q4.int8_quantize_rows(w)
         return cls(codes, scale, lin.bias, compute_dtype)
 

@@ -89,6 +89,7 @@ def library():
             "q4_gemm_grouped": ([i32, ctypes.POINTER(P), ctypes.POINTER(SP), ctypes.POINTER(P), i64,
                                  i32, i32, P, ctypes.c_size_t, P], i32),
             "q4_int8_quantize_rows": ([P, i32, i64, i64, i64, P, i64, P, P], i32),
+            "q4_int8_quantize_rows_f32": ([P, i64, i64, i64, P, i64, P, P], i32),
             "q4_int8_gemm_workspace_size": ([i64, i64, i64, ctypes.POINTER(sz)], i32),
             "q4_int8_gemm": ([P, i64, P, i64, P, i64, P, i64, i64, P, i32, P, i64, i32, P, sz, P], i32),
             "q4_int8_linear_scratch_size": ([i64, i64, ctypes.POINTER(sz)], i32),
@@ -558,12 +559,13 @@ def _rows16(x: torch.Tensor, name: str) -> torch.Tensor:
 
 
 def int8_quantize_rows(X: torch.Tensor, stream=None) -> tuple:
-    """(codes, scale) of a 2-D fp16/bf16 tensor: symmetric 8-bit codes with one
-    scale per row, X ~ codes * scale[:, None].  For a weight [N, K] (a scale
-    per output channel, once at load time) or for activations [M, K] (a scale
-    per token).  The code rows are padded to a multiple of 16 bytes: codes is
-    a [rows, K] view of that buffer."""
-    _rows16(X, "X")
+    """(codes, scale) of a 2-D fp16/bf16/fp32 tensor: symmetric 8-bit codes with
+    one scale per row, X ~ codes * scale[:, None].  For a weight [N, K] (a
+    scale per output channel, once at load time) or for activations [M, K] (a
+    scale per token).  The code rows are padded to a multiple of 16 bytes:
+    codes is a [rows, K] view of that buffer."""
+    if X.dtype not in _DT:
+        raise Q4Error(f"X must be float16, bfloat16 or float32, got {X.dtype}")
     if X.dim() != 2:
         raise Q4Error("X must be 2-D")
     rows, K = X.shape
@@ -579,9 +581,13 @@ def int8_quantize_rows(X: torch.Tensor, stream=None) -> tuple:
     codes = torch.empty(rows, ldc, dtype=torch.int8, device=X.device)[:, :K]
     scale = torch.empty(rows, dtype=torch.float32, device=X.device)
     if rows:
-        _check(library().q4_int8_quantize_rows(X.data_ptr(), _DT[X.dtype], rows, K, max(X.stride(0), K),
-                                               codes.data_ptr(), ldc, scale.data_ptr(), _current_stream(X)),
-               "q4_int8_quantize_rows")
+        ldx, s = max(X.stride(0), K), _current_stream(X)
+        if X.dtype == torch.float32:
+            _check(library().q4_int8_quantize_rows_f32(X.data_ptr(), rows, K, ldx, codes.data_ptr(), ldc,
+                                                       scale.data_ptr(), s), "q4_int8_quantize_rows_f32")
+        else:
+            _check(library().q4_int8_quantize_rows(X.data_ptr(), _DT[X.dtype], rows, K, ldx, codes.data_ptr(), ldc,
+                                                   scale.data_ptr(), s), "q4_int8_quantize_rows")
     return codes, scale
 
 

@@ -353,6 +353,10 @@ Q4_API int q4_gemm_grouped(int32_t count, const void *const *A, const q4_state *
 #define Q4_INT8_MAX_K 131071 /* K 128^2 < 2^31: no int8 operands overflow the 32-bit sums */
 Q4_API int q4_int8_quantize_rows(const void *X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ldx,
                                  int8_t *codes, int64_t ldc, float *scale, void *stream);
+/* The same for rows of binary32 (a checkpoint's weights, whose bits beyond 16
+ * decide codes): codes clamped to -127 .. 127, which only a subnormal s needs. */
+Q4_API int q4_int8_quantize_rows_f32(const float *X, int64_t rows, int64_t cols, int64_t ldx, int8_t *codes,
+                                     int64_t ldc, float *scale, void *stream);
 
 /*
  * q4_int8_gemm -- Y[M, N] = a_scale[m] w_scale[n] sum_k A[m, k] W[n, k] + bias[n]:

@@ -1,8 +1,9 @@
 """The 8-bit integer linear layer on a B200 at the borders of its kernels' ranges."""
+import numpy as np
 import pytest
 import torch
 
-from test_int8_gpu import q4  # noqa: F401  (the fixture)
+from test_int8_gpu import q4, rows_reference  # noqa: F401  (q4: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +24,47 @@ def test_linear_at_the_longest_rows_of_the_one_launch_kernel(q4, M, most, past):
         assert torch.equal(y, want.to(out))
     assert q4.last_device_status() == 0
 
+
+@pytest.mark.parametrize("K", [1, 64, 1001, 4104, 28672])
+def test_float32_rows_are_quantized_with_all_their_bits(q4, K):
+    """A checkpoint's float32 weights: the definition's codes and scales, not those of the weights in 16 bits."""
+    g = torch.Generator().manual_seed(K)
+    w = torch.randn(37, K, generator=g) * torch.exp(3 * torch.randn(37, 1, generator=g))
+    w[3] = 0
+    w[5] *= 1e-36
+    w[7] = 2.0 ** -140
+    codes, scale = q4.int8_quantize_rows(w.cuda())
+    want, s = rows_reference(w)
+    assert s[7] == 4 * 2.0 ** -149  # 2^-140 / 127, rounded to a subnormal: the quotient is 128
+    want[7] = 127
+    assert np.array_equal(scale.cpu().numpy(), s) and np.array_equal(codes.cpu().numpy(), want)
+    codes, scale = q4.int8_quantize_rows(w.cuda().t().contiguous().t())  # columns first: copied
+    assert np.array_equal(codes.cpu().numpy(), want)
+    if K > 9:
+        view = w[::2, 3:K - 2]
+        codes, scale = q4.int8_quantize_rows(w.cuda()[::2, 3:K - 2])
+        want, s = rows_reference(view)
+        assert np.array_equal(scale.cpu().numpy(), s) and np.array_equal(codes.cpu().numpy(), want)
+    assert q4.last_device_status() == 0
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_float32_row_that_is_not_finite_spoils_itself_alone(q4, bad):
+    w = torch.ones(3, 700, device="cuda")
+    w[1, 699] = bad
+    codes, scale = q4.int8_quantize_rows(w)
+    assert torch.isnan(scale).tolist() == [False, True, False] and not codes[1].any() and (codes[::2] == 127).all()
+    assert q4.last_device_status() == 1
+    q4.clear_device_status()
+
+
+def test_linear8bit_quantizes_float32_weights_themselves(q4):
+    from bit_blockwise_weight_absmax_b200 import linear8bit
+    torch.manual_seed(1)
+    lin = torch.nn.Linear(777, 130).cuda()
+    m = linear8bit.Linear8bit.from_linear(lin)
+    want, s = rows_reference(lin.weight)
+    assert np.array_equal(m.scale.cpu().numpy(), s) and np.array_equal(m.codes[:, :777].cpu().numpy(), want)
+    # half a step of a code for each weight, and no more
+    back = m.codes[:, :777].double() * m.scale.double()[:, None]
+    assert ((back - lin.weight.double()).abs() <= m.scale.double()[:, None] * (0.5 + 127 * 2.0 ** -23)).all()
