@@ -16,7 +16,10 @@ inline bool in16(int d) { return d == Q4_F16 || d == Q4_BF16; }
 inline bool any_float(int d) { return d == Q4_F16 || d == Q4_BF16 || d == Q4_F32; }
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 constexpr int64_t kMaxRows = INT32_MAX;
+// Of a product: a row number plus a tile or a grid's stride of rows stays within 32 bits.
+constexpr int64_t kMaxLinearRows = Q4_INT8_MAX_ROWS;
 constexpr int64_t kMaxKeys = (int64_t)1 << 30;  // of a sequence: positions and windows stay within 32 bits
+constexpr int64_t kMaxQueries = (int64_t)1 << 30;  // rows in front of position 0, less a window, do too
 constexpr int kDefaultSms = 148;  // sizes asked for without a device are those of a B200
 int plan_sms() {
   const DeviceInfo di = device_info();
@@ -24,7 +27,7 @@ int plan_sms() {
 }
 
 int check_linear(int64_t M, int64_t N, int64_t K) {
-  if (M < 1 || N < 1 || K < 1 || M > kMaxRows || N > kMaxRows || K > Q4_INT8_MAX_K) return Q4_ERR_SHAPE;
+  if (M < 1 || N < 1 || K < 1 || M > kMaxLinearRows || N > kMaxLinearRows || K > Q4_INT8_MAX_K) return Q4_ERR_SHAPE;
   return Q4_OK;
 }
 
@@ -225,7 +228,7 @@ int q4_kv_attention_workspace_size(const q4_kv_cache *cache, int64_t batch, int6
   if (!bytes) return Q4_ERR_ARG;
   const int rc = check_cache(cache, &v);
   if (rc != Q4_OK) return rc;
-  if (batch < 1 || batch > 65535 || total_q < 1 || total_q > kMaxRows || q_heads < 1 || q_heads % v.heads) return Q4_ERR_SHAPE;
+  if (batch < 1 || batch > 65535 || total_q < 1 || total_q > kMaxQueries || q_heads < 1 || q_heads % v.heads) return Q4_ERR_SHAPE;
   *bytes = kv_attention_ws(cache->head_dim, plan_sms());
   return Q4_OK;
 }
@@ -268,7 +271,8 @@ int q4_kv_attention(const q4_kv_cache *cache, const void *Q, int32_t dtype, int6
   p.sms = di.sms;
   p.stall_copies = g_copy_stall.load(std::memory_order_relaxed);
   p.status = di.status;
-  return run_kv_attention(dtype, cache->head_dim, cache->blocksize, p, max_q, di.sms, (cudaStream_t)stream);
+  return run_kv_attention(dtype, cache->head_dim, cache->blocksize, p, std::min(max_q, total_q), di.sms,
+                          (cudaStream_t)stream);
 }
 
 }  // extern "C"

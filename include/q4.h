@@ -351,6 +351,7 @@ Q4_API int q4_gemm_grouped(int32_t count, const void *const *A, const q4_state *
  * Q4_ERR_SHAPE for rows < 1, cols < 1, cols > Q4_INT8_MAX_K or a short stride.
  */
 #define Q4_INT8_MAX_K 131071 /* K 128^2 < 2^31: no int8 operands overflow the 32-bit sums */
+#define Q4_INT8_MAX_ROWS 2147418112 /* 2^31 - 2^16, of a product's M and N */
 Q4_API int q4_int8_quantize_rows(const void *X, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ldx,
                                  int8_t *codes, int64_t ldc, float *scale, void *stream);
 /* The same for rows of binary32 (a checkpoint's weights, whose bits beyond 16
@@ -362,7 +363,7 @@ Q4_API int q4_int8_quantize_rows_f32(const float *X, int64_t rows, int64_t cols,
  * q4_int8_gemm -- Y[M, N] = a_scale[m] w_scale[n] sum_k A[m, k] W[n, k] + bias[n]:
  * the sum in 32-bit integers (exact), then binary32 (the sum times the product
  * of the two scales, plus the bias, each rounded) and one rounding to y_dtype,
- * for any M, N >= 1 and 1 <= K <= Q4_INT8_MAX_K.
+ * for 1 <= M, N <= Q4_INT8_MAX_ROWS and 1 <= K <= Q4_INT8_MAX_K.
  *   A, W   device, int8, 16-byte aligned, rows lda / ldw bytes apart
  *          (multiples of 16, >= K); what lies past K is not read into a sum.
  *   bias   device, [N] of bias_dtype (Q4_F16 / Q4_BF16 / Q4_F32), or NULL.
@@ -476,7 +477,7 @@ Q4_API int q4_kv_dequantize(const q4_kv_cache *cache, const int64_t *slots, int6
  *   max_q  the most rows of any sequence: it only helps to choose the kernel.
  *   workspace  as q4_int8_gemm's, q4_kv_attention_workspace_size() bytes (the
  *          two may share one).
- * batch at most 65535.  Entries outside the cache, lengths outside the table
+ * batch at most 65535, total_q at most 2^30.  Entries outside the cache, lengths outside the table
  * and row ranges outside Q are cut off and set Q4_STATUS_INDEX; where ranges
  * overlap, the rows of either may be left out.  The order of every sum is fixed by
  * the arguments and the device: identical calls give identical bits.

@@ -1,9 +1,12 @@
 """The serving operators without a GPU: refusals at the borders of their ranges."""
+import ctypes
+
 import pytest
 import torch
 
 from bit_blockwise_weight_absmax_b200 import q4
 from test_int8_cpu import ALIGN, ARG, NO_DEVICE, SHAPE, A, lib  # noqa: F401  (lib: the fixture)
+from test_kv_cpu import cache
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="made-up pointers: only where nothing can be launched")
@@ -22,3 +25,14 @@ def test_other_types_are_refused():
     for dtype in (torch.float64, torch.int8):
         with pytest.raises(q4.Q4Error, match="float32"):
             q4.int8_quantize_rows(torch.zeros(2, 64, dtype=dtype))
+
+
+def test_sizes_whose_row_numbers_would_leave_32_bits_are_refused(lib):
+    """A product's last row plus the rows that a grid takes at once; a query row in front of every key less a window."""
+    n = ctypes.c_size_t(0)
+    most = 2 ** 31 - 2 ** 16
+    for M, N, rc in ((1, most, 0), (1, most + 1, SHAPE), (1, 2 ** 31 - 1, SHAPE), (most, 1, 0), (most + 1, 1, SHAPE)):
+        assert lib.q4_int8_gemm_workspace_size(M, N, 16, ctypes.byref(n)) == rc
+        assert lib.q4_int8_linear_scratch_size(M, 16, ctypes.byref(n)) == (SHAPE if M > most else 0)
+    for total, rc in ((2 ** 30, 0), (2 ** 30 + 1, SHAPE), (2 ** 31 - 1, SHAPE)):
+        assert lib.q4_kv_attention_workspace_size(cache(), 4, total, 8, ctypes.byref(n)) == rc
