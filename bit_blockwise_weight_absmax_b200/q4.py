@@ -830,8 +830,9 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq
     keys; seq_lens int32 [batch], keys of each sequence, those of its query
     rows included.  cu_seqlens_q int32 [batch + 1]: sequence b has the rows
     cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1, its last ones; None: one row
-    each (rows = batch).  max_q: the most rows of a sequence, a hint (default:
-    rows of the whole call when cu_seqlens_q is given).  scale: 1 /
+    each (rows = batch).  max_q: the most rows of a sequence, a hint that
+    chooses the kernel (default: 1 where there are as many rows as sequences,
+    else the rows of the whole call).  scale: 1 /
     sqrt(head_dim) unless given.  causal: a row attends to the keys up to its
     own position; window > 0: only to the last `window` of them.  Rows that
     attend to nothing are zero, with log sum exp -inf; rows outside
@@ -888,7 +889,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, seq
         s = _current_stream(q)
         ws, ws_bytes, _ = _stream_workspace(dev, s, need)
         if max_q is None:
-            max_q = 1 if cu_seqlens_q is None else rows
+            max_q = 1 if cu_seqlens_q is None or rows == batch else rows
         _check(library().q4_kv_attention(
             cache._ref, q.data_ptr(), _DT[q.dtype], rows, heads, qt, qh,
             None if cu_seqlens_q is None else cu_seqlens_q.data_ptr(), seq_lens.data_ptr(),

@@ -146,3 +146,15 @@ def test_a_block_that_could_not_be_held_spoils_whole_rows_in_either_kernel(q4, D
             assert torch.isnan(t).all()
         for t in (out[:rows, :2], out[rows:], lse[:rows, :2], lse[rows:]):
             assert torch.isfinite(t).all()
+
+
+def test_the_hint_left_out_takes_the_kernel_for_few_rows_where_the_rows_are_as_many_as_the_sequences(q4):
+    """A decode step given by its row ranges: the same kernel, and so the same bits, as with the hint 1."""
+    g = torch.Generator().manual_seed(3)
+    lens = [(37 * b) % 900 + 1 for b in range(64)]
+    c, table = fill_cache(q4, g, lens, 2, 128, 64, 64)
+    q = torch.randn(64, 8, 128, generator=g).half().cuda()
+    args = (q, c, table.cuda(), ints(lens), torch.arange(65, dtype=torch.int32, device="cuda"))
+    want = q4.kv_attention(*args, max_q=1)
+    assert not torch.equal(q4.kv_attention(*args, max_q=64), want)  # the other kernel rounds otherwise
+    assert torch.equal(q4.kv_attention(*args), want)
