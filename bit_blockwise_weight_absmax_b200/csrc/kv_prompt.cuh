@@ -10,7 +10,7 @@
 //                 them.  The reference m of 2^(score - m) stays that of earlier
 //                 tiles while the weights fit binary16 (their sum tells); only
 //                 then, and for the first tile, the maximum is taken, the
-//                 reference set kKpLift below it and the output rescaled: one
+//                 reference set kp_lift() below it and the output rescaled: one
 //                 pass over the scores in the common case;
 //   warps 8..11   dequantize: a thread owns a key.  Codes come straight from
 //                 global memory into registers, a tile ahead; 1024 + code is
@@ -43,10 +43,14 @@ constexpr int kKpRows = 256;   // query rows of a CTA
 constexpr int kKpKeys = 128;   // keys of a tile
 constexpr int kKpThreads = 512;
 constexpr int kKpMinTiles = 4;         // key tiles a CTA takes of a tile that several share, at least
-// The reference is taken kKpLift below the maximum: the largest weight is 2^8
-// then, those of 2^-22 of it have all of binary16's bits, and below 2^-33 they
-// are dropped (64 equal ones sum up to 2^14, well inside kKpMost).
-constexpr float kKpLift = 8.0f;
+// The reference is taken kp_lift() below the maximum: the largest weight is
+// 2^lift then, and a binary16 weight is off by 2^-25 at most below the normal
+// range, so n keys by n 2^(-25 - lift) of the largest: less than 2^-16 up to 2^17
+// keys (2^-13 up to 2^20).  64 equal weights of 2^8 sum up to 2^14, inside
+// kKpMost.  Not more than the keys need: rows whose scores climb past the
+// headroom take the maximum again (2048 rows over 8192 keys, scores of a standard
+// deviation of 3: 530 us with this rule's 4, 508 with 0, 738 with 8).
+__device__ __forceinline__ float kp_lift(int keys) { return (float)min(8, max(0, 32 - __clz(max(keys - 1, 0)) - 9)); }
 constexpr float kKpAhead = 15.0f;    // scores up to this far past the reference keep it
 constexpr float kKpMost = 65504.0f;  // of a row's weights in a tile: each is inside binary16 then
 
@@ -300,6 +304,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
     const uint32_t ot = o_addr + (uint32_t)(half * D) + ((uint32_t)((warp & 3) * 32) << 16);
     float m = -INFINITY, l = 0.0f;
     const uint64_t hf2 = f2_pack(hf, hf);
+    const float lift = kp_lift(tiles * kKpKeys);
     bool ok = true, fresh = true;  // fresh: a row of the warp has no reference yet
     for (int j = 0; j < tiles && ok; ++j) {
       // the whole warp goes on or none of it: what follows are its collectives
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
           for (int k = 0; k < 64; ++k) top = fmaxf(top, __uint_as_float(s[k >> 5][k & 31]));
           top *= hf;
           if (fresh) move = !(top <= m + kKpAhead);
-          top = fmaxf(m, top - kKpLift);
+          top = fmaxf(m, top - lift);
           const float f = !move || m == -INFINITY ? 1.0f : ex2(m - top);
           if (move) m = top, l *= f;
           if ((j | u) && __any_sync(0xffffffffu, f != 1.0f)) {

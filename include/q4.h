@@ -469,11 +469,11 @@ Q4_API int q4_kv_dequantize(const q4_kv_cache *cache, const int64_t *slots, int6
  *          scores, or NULL.  Where it is asked for, prompts multiply the keys
  *          with all their bits (else rounded to binary16, a fifth faster over
  *          long ones): `out` may differ in its last bits between the two.
- *          Weights are rounded to binary16 (sums and statistics are binary32):
- *          those of 2^-22 of a row's largest at least keep 11 bits, those below
- *          2^-33 of it are dropped from `out`.  (Few rows weigh a value with its
- *          scale: where the scales of a vector's two blocks lie more than 2^24
- *          apart, the smaller block's values lose bits.)
+ *          Weights are rounded to binary16 (sums and statistics are binary32),
+ *          scaled so that what small ones lose is less than 2^-16 of a row's
+ *          largest weight in all up to 2^17 keys, 2^-13 up to 2^20.  (Few rows
+ *          weigh a value with its scale: where the scales of a vector's two blocks
+ *          lie more than 2^24 apart, the smaller block's values lose bits.)
  *   max_q  the most rows of any sequence: it only helps to choose the kernel.
  *   workspace  as q4_int8_gemm's, q4_kv_attention_workspace_size() bytes (the
  *          two may share one).
