@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_kv_gpu import HALF, check, fill_cache, q4  # noqa: F401  (q4: the fixture)
+from gpu_helpers import bits, is_bf16
+from test_kv_gpu import HALF, INDEX, check, fill_cache, q4, reference, values  # noqa: F401  (q4: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -158,3 +159,120 @@ def test_the_hint_left_out_takes_the_kernel_for_few_rows_where_the_rows_are_as_m
     want = q4.kv_attention(*args, max_q=1)
     assert not torch.equal(q4.kv_attention(*args, max_q=64), want)  # the other kernel rounds otherwise
     assert torch.equal(q4.kv_attention(*args), want)
+
+
+@pytest.mark.parametrize("D,B,qh,kh", [(64, 64, 9, 3), (128, 64, 8, 2), (128, 128, 4, 4)])
+@pytest.mark.parametrize("max_q", [1, 3, 10 ** 6])
+def test_a_hint_that_is_off_changes_no_result(q4, D, B, qh, kh, max_q):
+    """Either kernel takes any rows: many row tiles of a sequence in the one for few, single rows in the one for many."""
+    g = torch.Generator().manual_seed(D + B)
+    for lens, qs in (([64, 900, 2, 333], [64, 450, 1, 333]), ([200, 1, 90], [1, 1, 1])):
+        c, table = fill_cache(q4, g, lens, kh, D, B, 32)
+        q = torch.randn(sum(qs), qh, D, generator=g).half()
+        cu = ints([0] + list(np.cumsum(qs)))
+        out, lse = q4.kv_attention(q.cuda(), c, table.cuda(), ints(lens), cu, max_q=max_q, return_lse=True)
+        ref, rl, tol, ltol = reference(c, table, lens, qs, q, D ** -0.5, True, 0)
+        assert ((out.double().cpu() - ref).abs() <= tol + HALF[q.dtype] * (ref.abs() + tol) + 2.0 ** -25).all()
+        assert ((lse.double().cpu() - rl).abs() <= ltol).all()
+    assert q4.last_device_status() == 0
+
+
+@pytest.mark.parametrize("D,B", [(64, 64), (128, 64), (128, 128)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_calls_of_many_tokens_write_and_read_the_same_bits(q4, oracle, D, B, dtype):
+    """Threads take several tokens each; slots outside the cache near the end, where a thread's tokens run out."""
+    T, H, page = 8191, 32, 64
+    g = torch.Generator().manual_seed(D + B)
+    k, v = (torch.randn(T, H, D, generator=g).to(dtype) for _ in range(2))
+    pages = T // page + 3
+    c = q4.kv_cache(pages, H, D, page, B)
+    for t in (c.k_codes, c.v_codes):
+        t.fill_(0xAB)
+    slots = torch.randperm(pages * page, generator=g)[:T]
+    for at, slot in ((0, -1), (63, -5), (T - 130, -1), (T - 65, pages * page), (T - 2, -1), (T - 1, pages * page + 7)):
+        slots[at] = slot
+    q4.kv_append(c, k.cuda(), v.cuda(), slots.cuda())
+    assert q4.last_device_status() == INDEX
+    q4.clear_device_status()
+    some = (slots >= 0) & (slots < pages * page)
+    for x, codes, state in ((k, c.k_codes, c.k_state), (v, c.v_codes, c.v_state)):
+        ost = oracle.quantize(bits(x), is_bf16(x), B, oracle.QT_INT4_ASYM, False, True)
+        nb = D // B
+        z = np.empty(2 * ost.zero.size, dtype=np.uint8)
+        z[0::2], z[1::2] = ost.zero & 15, ost.zero >> 4
+        s = ost.scale_f16_bits().view(np.float16).reshape(T, H, nb)[some]
+        got = state.cpu().numpy().transpose(0, 2, 1, 3, 4).reshape(-1, H, nb, 2)
+        at = slots[some].numpy()
+        assert np.array_equal(got[at][..., 0], s)
+        assert np.array_equal(got[at][..., 1], z[:T * H * nb].reshape(T, H, nb)[some])
+        want = ost.codes().reshape(T, H, nb, B // 8, 8).swapaxes(2, 3).reshape(T, H, D // 2, 2)[some]
+        got = codes.cpu().numpy().transpose(0, 2, 1, 3).reshape(-1, H, D // 2)
+        assert np.array_equal(got[at], want[..., 0] | (want[..., 1] << 4))
+        rest = np.ones(pages * page, dtype=bool)
+        rest[at] = False
+        assert (got[rest] == 0xAB).all()
+    for out in (torch.float16, torch.bfloat16):
+        for x, codes, state in zip(q4.kv_dequantize(c, slots.cuda(), out), (c.k_codes, c.v_codes), (c.k_state, c.v_state)):
+            flat_c, flat_s = (t.cpu().transpose(1, 2).flatten(0, 1) for t in (codes, state))
+            assert torch.equal(x.cpu()[some], values(flat_c[slots[some]], flat_s[slots[some]]).to(out))
+            assert not x.cpu()[~some].any()
+    assert q4.last_device_status() == INDEX
+    q4.clear_device_status()
+
+
+@pytest.mark.parametrize("D,B", [(64, 64), (128, 64), (128, 128)])
+@pytest.mark.parametrize("window", [1, 0])
+@pytest.mark.parametrize("few", [False, True])
+def test_the_log_sum_exp_has_all_bits_of_the_keys(q4, D, B, window, few):
+    """Queries along what rounding their own keys to binary16 leaves over, where the rounding costs most.  The bound has
+    binary32 terms alone.  An MMA adds 16 products to its sum, each cut at the last bit of the largest (17 terms, a step
+    of 2^-23 of at most sum |q k| each); many rows take D / 16 MMAs for the rounded keys and as many for what is left.
+    Few rows sum code - 8 and take (z - 8) sum(q) off, each up to 8 s |q| (a window's units lie at the ends of its
+    keys; whole units sum the codes, and z, up to 15).  Then a dozen roundings of the score in base 2, exponentials
+    and logarithm (2^-21), and the sum over n keys, n / 64 + 20 additions in a row."""
+    n, H = 300, 2
+    g = torch.Generator().manual_seed(D + B + window)
+    c, table = fill_cache(q4, g, [n], H, D, B, 64)
+    at = table[0, torch.arange(n) // 64].long(), torch.arange(n) % 64
+    k = values(c.k_codes, c.k_state)[at[0], :, at[1]]  # [n, H, D]
+    s = c.k_state.cpu().double()[at[0], :, at[1]][..., 0].repeat_interleave(B, -1)
+    rest = k - k.half().double()
+    q = torch.where(rest != 0, rest.sign(), torch.randn(n, H, D, generator=g).sign().double())
+    q = (q * (1 + torch.randint(0, 8, q.shape, generator=g) / 8)).half()
+    lse = q4.kv_attention(q.cuda(), c, table.cuda(), ints([n]), ints([0, n]), max_q=1 if few else n, window=window,
+                          return_lse=True)[1].double().cpu()
+    scale = D ** -0.5
+    seen = torch.ones(n, n).tril().bool() & (torch.ones(n, n).triu().bool() if window else True)
+    step = 2.0 ** -23
+    for h in range(H):
+        qh = q[:, h].double()
+        want = torch.logsumexp((qh @ k[:, h].t() * scale).masked_fill(~seen, -math.inf), 1)
+        if few:
+            most = 8 if window else 15
+            off = most * (D / 16 * 17 * step + (D + 4) * step / 2) * (qh.abs() @ s[:, h].t())
+        else:
+            off = D / 8 * 17 * step * (qh.abs() @ k[:, h].abs().t())
+        x = qh @ k[:, h].t() * scale
+        tol = scale * torch.where(seen, off, 0.0).amax(1) + 12 * step / 2 * (1.45 * torch.where(seen, x.abs(), 0.0).amax(1) + 16)
+        tol += 2.0 ** -21 + (0 if window else (n / 64 + 20) * step / 2)
+        assert ((lse[:, h] - want).abs() <= tol).all(), ((lse[:, h] - want).abs() / tol).max()
+        if window and not few:  # keys rounded to binary16 would not pass
+            lost = scale * (qh * rest[:, h]).sum(1).abs()
+            assert (lost > tol).double().mean() > 0.5
+    assert q4.last_device_status() == 0
+
+
+@pytest.mark.parametrize("D,B,qh,kh", [(64, 64, 9, 3), (128, 64, 8, 2), (128, 128, 4, 4)])
+@pytest.mark.parametrize("lens,qs", [([129, 600], [129, 300]), ([9000], [260]), ([700] * 20, [3] * 20)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 100)])
+def test_the_call_without_the_log_sum_exp(q4, D, B, qh, kh, lens, qs, causal, window):
+    """The default: prompts run another loop, with the keys rounded to binary16 (inside the reference's bound)."""
+    g = torch.Generator().manual_seed(sum(lens) + D)
+    dtype = torch.float16 if B == 64 else torch.bfloat16
+    c, table = fill_cache(q4, g, lens, kh, D, B, 64, dtype)
+    q = torch.randn(sum(qs), qh, D, generator=g).to(dtype)
+    out = q4.kv_attention(q.cuda(), c, table.cuda(), ints(lens), ints([0] + list(np.cumsum(qs))), max_q=max(qs),
+                          causal=causal, window=window)
+    ref, _, tol, _ = reference(c, table, lens, qs, q, D ** -0.5, causal, window)
+    assert ((out.double().cpu() - ref).abs() <= tol + HALF[dtype] * (ref.abs() + tol) + 2.0 ** -25).all()
+    assert q4.last_device_status() == 0
