@@ -330,12 +330,14 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
           }
         }
       }
-      // every copy completes before the CTA (the pair, see the end) may exit
+      // every copy completes before the CTA (the pair, see the end) may exit; a
+      // pair's stages stay unfilled where the other CTA gave up before it copied
       if (rank == 0 && !p.stall_copies)
         for (uint32_t j = i > S ? i - S : 0; j < i; ++j) {
-          int dummy = 0;
           volatile int no_abort = 0;
-          mbar_wait(full_bar(j % S), (j / S) & 1, &dummy, &no_abort);
+          if (!mbar_wait(full_bar(j % S), (j / S) & 1, PAIR ? p.status : nullptr, PAIR ? abort : &no_abort,
+                         PAIR ? p.wait_ns : kWaitLimitNs))
+            break;
         }
     }
   } else if (warp == 1) {
@@ -372,9 +374,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
       }
       // every MMA issued completes before TMEM is freed, also after a timeout
       if (committed) {
-        int dummy = 0;
         volatile int no_abort = 0;
-        mbar_wait(last_bar, last_par, &dummy, &no_abort);
+        mbar_wait(last_bar, last_par, nullptr, &no_abort);
       }
     }
   } else {
@@ -497,9 +498,9 @@ __global__ void __launch_bounds__(kI8Threads, 1) int8_gemm_kernel(const __grid_c
   }
 
   if (PAIR && *abort && warp == 0 && lane == 0) {
-    // after a timeout the CTA that does not own the stage barriers cannot
-    // wait for its copies on them: it gives them a millisecond (they take
-    // microseconds) before the pair ends
+    // after a timeout a pair's CTAs cannot wait for their copies on the stage
+    // barriers, which may lack the other's: they give them a millisecond (they
+    // take microseconds) before the pair ends
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
   }

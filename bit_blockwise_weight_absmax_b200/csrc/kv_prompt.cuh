@@ -667,9 +667,8 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
       else products(std::false_type{});
       // every MMA issued completes before TMEM is freed, also after a timeout
       if (committed) {
-        int dummy = 0;
         volatile int no_abort = 0;
-        mbar_wait(last_bar, last_par, &dummy, &no_abort);
+        mbar_wait(last_bar, last_par, nullptr, &no_abort);
       }
     }
   }

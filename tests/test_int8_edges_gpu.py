@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_int8_gpu import q4, rows_reference  # noqa: F401  (q4: the fixture)
+from test_int8_gpu import q4, random_codes, rows_reference  # noqa: F401  (q4: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,28 @@ def test_linear8bit_quantizes_float32_weights_themselves(q4):
     # half a step of a code for each weight, and no more
     back = m.codes[:, :777].double() * m.scale.double()[:, None]
     assert ((back - lin.weight.double()).abs() <= m.scale.double()[:, None] * (0.5 + 127 * 2.0 ** -23)).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(9, 600, 4096), (100, 4096, 4096), (1024, 1024, 8192), (3000, 4096, 2048)])
+def test_waits_that_run_out_while_copies_are_on_their_way(q4, M, N, K):
+    """Limits around a copy's own time, single CTAs and pairs: any wait may run out (a probe of a barrier blocks for a
+    while itself, so none has to).  Every call returns, with the right result or with its status, and the next is right."""
+    g = torch.Generator().manual_seed(M)
+    A, sa = random_codes(g, M, K)
+    W, sw = random_codes(g, N, K)
+    want = q4.int8_gemm(A, sa, W, sw, None, torch.float32)
+    try:
+        for limit in (1, 300, 1000, 2000, 5000) * 4:
+            q4.set_wait_limit_ns(limit)
+            y = q4.int8_gemm(A, sa, W, sw, None, torch.float32)
+            torch.cuda.synchronize()
+            status = q4.last_device_status()
+            assert status in (0, 2)
+            assert status or torch.equal(y, want)
+            q4.reset_workspaces()
+            q4.clear_device_status()
+    finally:
+        q4.set_wait_limit_ns(0)
+        q4.reset_workspaces()
+        q4.clear_device_status()
+    assert torch.equal(q4.int8_gemm(A, sa, W, sw, None, torch.float32), want)
