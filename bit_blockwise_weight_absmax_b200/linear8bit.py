@@ -29,7 +29,14 @@ class Linear8bit(torch.nn.Module):
             raise q4.Q4Error(f"Linear8bit cannot run this layer: {why}")
         self.compute_dtype = compute_dtype
         # the whole padded rows are the buffer: module copies and moves keep them
-        self.register_buffer("codes", codes.as_strided((codes.shape[0], codes.stride(0)), (codes.stride(0), 1)))
+        rows, ld = codes.shape[0], (codes.shape[1] + 15) // 16 * 16
+        if codes.stride(0) == ld and codes.storage_offset() + rows * ld <= codes.untyped_storage().nbytes():
+            codes = codes.as_strided((rows, ld), (ld, 1))
+        else:  # part of a wider buffer
+            padded = codes.new_zeros(rows, ld)
+            padded[:, :self.in_features] = codes
+            codes = padded
+        self.register_buffer("codes", codes)
         self.register_buffer("scale", scale)
         self.bias = None if bias is None else torch.nn.Parameter(bias.detach().to(compute_dtype), requires_grad=False)
 
@@ -49,7 +56,10 @@ class Linear8bit(torch.nn.Module):
         if x.shape[-1] != self.in_features:
             raise q4.Q4Error(f"expected last dimension {self.in_features}, got {x.shape[-1]}")
         a = x.reshape(-1, self.in_features).to(self.compute_dtype)
-        y = q4.int8_linear(a, self.codes[:, :self.in_features], self.scale, self.bias)
+        bias = self.bias
+        if bias is not None and bias.dtype == torch.float64:  # model.double()
+            bias = bias.float()
+        y = q4.int8_linear(a, self.codes[:, :self.in_features], self.scale, bias)
         return y.reshape(*x.shape[:-1], self.out_features)
 
     def _apply(self, fn, recurse=True):

@@ -93,3 +93,15 @@ def test_waits_that_run_out_while_copies_are_on_their_way(q4, M, N, K):
         q4.reset_workspaces()
         q4.clear_device_status()
     assert torch.equal(q4.int8_gemm(A, sa, W, sw, None, torch.float32), want)
+
+
+def test_linear8bit_after_casts_of_the_model(q4):
+    """The codes and scales stay as they are; a bias of any type is added in binary32."""
+    from bit_blockwise_weight_absmax_b200 import linear8bit
+    torch.manual_seed(2)
+    m = linear8bit.Linear8bit.from_linear(torch.nn.Linear(300, 70).cuda(), torch.float16)
+    x = torch.randn(6, 300, device="cuda").half()
+    want = m(x)
+    for cast in ("half", "double", "float"):
+        getattr(m, cast)()
+        assert torch.equal(m(x), want)

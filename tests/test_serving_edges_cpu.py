@@ -4,7 +4,7 @@ import ctypes
 import pytest
 import torch
 
-from bit_blockwise_weight_absmax_b200 import q4
+from bit_blockwise_weight_absmax_b200 import linear8bit, q4
 from test_int8_cpu import ALIGN, ARG, NO_DEVICE, SHAPE, A, lib  # noqa: F401  (lib: the fixture)
 from test_kv_cpu import cache
 
@@ -36,3 +36,10 @@ def test_sizes_whose_row_numbers_would_leave_32_bits_are_refused(lib):
         assert lib.q4_int8_linear_scratch_size(M, 16, ctypes.byref(n)) == (SHAPE if M > most else 0)
     for total, rc in ((2 ** 30, 0), (2 ** 30 + 1, SHAPE), (2 ** 31 - 1, SHAPE)):
         assert lib.q4_kv_attention_workspace_size(cache(), 4, total, 8, ctypes.byref(n)) == rc
+
+
+def test_linear8bit_takes_codes_that_are_part_of_a_wider_buffer():
+    wide = torch.randint(-127, 128, (5, 96), dtype=torch.int8)
+    for codes in (wide[:, 16:80], wide[:, :64], wide[:, 32:86], wide[1:2, 16:80], wide[::2, 80:], wide[:, 16:]):
+        m = linear8bit.Linear8bit(codes, torch.ones(codes.shape[0]))
+        assert torch.equal(m.codes[:, :m.in_features], codes) and m.codes.shape[1] == (codes.shape[1] + 15) // 16 * 16
