@@ -31,7 +31,7 @@
 // previous kernel, so they travel while that kernel (the quantization of the
 // tokens) still runs; a prefetch changes nothing, so weights that an earlier
 // kernel is still writing are read correctly after the wait.
-// Measured: 4096 x 28672 x 8192 640 us (3.0 POP/s, tensor pipe busy 0.82 to
+// Measured: 4096 x 28672 x 8192 630 us (3.1 POP/s, tensor pipe busy 0.82 to
 // 0.90 of the time); 24 x 11008 x 4096 15.2 us (3.0 TB/s).
 // Every wait is bounded: a timeout raises Q4_STATUS_TIMEOUT and ends the
 // launch with undefined outputs (the workspace is then zero-filled again by

@@ -1,8 +1,9 @@
 // kv_attention.cuh -- softmax(scale Q K^T) V over the paged 4-bit cache: the
 // kernel for single and few query rows (sm_100a).
 //
-// Bound by the cache's bytes (D + 8 D / B per key and head) and, close behind,
-// by issue: so the codes go into the tensor cores as they are.
+// What it cannot do without are the cache's bytes (D + 8 D / B per key and
+// head); instructions come close behind (637 a warp and 32 keys, in 0.45 of the
+// issue slots), so the codes go into the tensor cores as they are.
 //  - A 4-bit code masked out of a packed word is a binary16 number already:
 //    w & 0x000f000f holds two codes as multiples of 2^-24 (binary16
 //    subnormals, which the MMAs take exactly), w & 0x00f000f0 two more times
@@ -32,7 +33,7 @@
 // tile below 128 rows on the key side that would pay for 8 query rows, and
 // needs dequantized operands in shared memory; here registers feed the MMAs.)
 // Measured: 100 keys 8.7 us; 16 sequences of up to 8192 keys, 64 heads over 8,
-// 45 us (2.2 TB/s); 131071 keys 56 us (2.7 TB/s); about 6 us before the first
+// 43 us (2.4 TB/s); 131071 keys 55 us (2.8 TB/s); about 6 us before the first
 // unit and 5 for a join are fixed, units stream at 4.7 TB/s between them.
 #pragma once
 #include <limits.h>
@@ -363,6 +364,9 @@ __device__ __forceinline__ void kv_unit(KvRun<D, B, NT> &run, const uint8_t *kc,
           lsum[n][0] += pr[0], lsum[n][1] += pr[1];
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
+            // rounded to binary16, the MMA's type beside the codes: half a step,
+            // 2^-11, as the output's own in binary16 (which is off by 2.1e-4 and
+            // 2.3e-4 in the norm, 2.1e-4 and 2.2e-4 with binary32 weights)
             ww[mt][n][j][h] = Dt<Q4_F16>::pack2(w[j][0], w[j][1]);
             top = __vmaxu2(top, ww[mt][n][j][h]);
           }

@@ -27,9 +27,8 @@
 // the last, partly filled wave are cut along the keys over the idle SMs, their
 // partial outputs joined by the CTA that comes last (few rows over many keys
 // are all such tiles).
-// Measured: 2048 rows of 64 heads over 8192 keys 510 us (940 TFLOP/s, tensor
-// pipe busy half the time), 650 with the log sum exp; 4096 rows of 32 heads
-// over their own keys 261 us with it.
+// Measured: 2048 rows of 64 heads over 8192 keys 538 us (894 TFLOP/s, tensor
+// pipe busy half the time), 674 with the log sum exp.
 // Tensor memory: two score tiles of 128 columns (weights over their first 64)
 // and two outputs of D.  Query rows are scaled by a power of two into binary16.
 #pragma once
@@ -239,7 +238,9 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
   // 16 bits itself and hardly shows it (relative error 2.1e-4 with exact keys,
   // 2.3e-4 with rounded ones, binary16), but the log sum exp does: 2e-6 over
   // 2000 keys, 2e-4 over one.  Where it is asked for, the remainders are
-  // multiplied too: 1e-7.
+  // multiplied too: 1e-7.  Values and weights are rounded to binary16 in any
+  // case, since the product takes no wider operands at its rate: binary16
+  // outputs are off by 2.5e-4 to 2.8e-4, 2.1e-4 with all in binary32.
   const bool exact = p.lse != nullptr;
   // this CTA's part of the keys
   const int parts = (int)blockIdx.x < whole ? 1 : max(1, min(share, tiles / kKpMinTiles));
