@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kKpThreads, 1) kv_prompt_kernel(const __grid_c
   // 2000 keys, 2e-4 over one.  Where it is asked for, the remainders are
   // multiplied too: 1e-7.  Values and weights are rounded to binary16 in any
   // case, since the product takes no wider operands at its rate: binary16
-  // outputs are off by 2.5e-4 to 2.8e-4, 2.1e-4 with all in binary32.
+  // outputs are off by 2.5e-4 to 2.9e-4, 2.1e-4 with all in binary32.
   const bool exact = p.lse != nullptr;
   // this CTA's part of the keys
   const int parts = (int)blockIdx.x < whole ? 1 : max(1, min(share, tiles / kKpMinTiles));
